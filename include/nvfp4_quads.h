@@ -272,7 +272,7 @@ NVFP4_API nvfp4_status nvfp4_qdq_weights(const void *w_dev, int64_t G, int64_t r
  *   topk_gate_dev float32 [T x k_r]: softmax over the k_r selected logits.
  *   seg_align    128 or 256: every expert segment is padded to a multiple of
  *                this many rows (the grouped GEMM's tile height: 256 selects
- *                its 2-SM shape).
+ *                its 2-SM shape).  1: no padding (moe_ragged_gemm).
  *   offsets_dev  int32 [E+1]: expert e owns routed rows
  *                [offsets[e], offsets[e+1]); offsets[E] = total padded rows.
  *   dst_row_dev  int32 [T x k_r]: routed row of (token t, slot j).  Inside
@@ -391,7 +391,8 @@ NVFP4_API nvfp4_status nvfp4_gather_weight_channels_cm_experts(const uint8_t *co
 typedef enum {
     MOE_EPI_STORE_F32 = 0,
     MOE_EPI_SWIGLU_BF16 = 1,
-    MOE_EPI_SCATTER_ADD_F32 = 2
+    MOE_EPI_SCATTER_ADD_F32 = 2,
+    MOE_EPI_COMBINE_F32 = 3           /* moe_nvfp4_gemv only */
 } moe_epilogue;
 
 NVFP4_API nvfp4_status moe_w4a4_grouped_gemm_rac(
@@ -487,6 +488,147 @@ NVFP4_API nvfp4_status moe_w8a8_grouped_gemm(
     const float *b_s_dev, int64_t N, int64_t K, int32_t E, const int32_t *offsets_dev, int32_t seg_align,
     int32_t epilogue, const int32_t *row_token_dev, const float *row_gate_dev, void *out_dev, int64_t ld_out,
     float *amax_out_dev, int32_t *dev_status, void *stream);
+
+/* --------------------------------------------------------------------------
+ * moe_ragged_gemm -- BF16 products grouped by expert over ragged row
+ * segments, forward and input gradient (the trainer side, gist.science/it
+ * 2.2 A: activations and gradients stay in BF16).  Expert e owns rows
+ * offsets[e] <= r < offsets[e+1]; segments have any length, zero included,
+ * and are not padded (moe_route with seg_align 1 gives such a layout).
+ *   transpose = 0:  out[r, n] = sum_k a[r, k] w[e, n, k]
+ *                   a bf16 [M x lda], K columns; out [M x ld_out], N columns
+ *   transpose = 1:  out[r, k] = sum_n a[r, n] w[e, n, k]
+ *                   a bf16 [M x lda], N columns; out [M x ld_out], K columns
+ *   w_dev        bf16 [E x N x K], contiguous.
+ *   offsets_dev  int32 [E+1], ascending, in [0, M].  Bounds outside that are
+ *                read as their running maximum clamped to [0, M].
+ *   out_dev      f32 (out_f32 != 0) or bf16; f32 accumulation, one rounding.
+ * Rows below offsets[0] or from offsets[E] on are neither read into a result
+ * nor written.  E <= 256, K % 8 == 0, lda % 8 == 0, any N, ld_out >= the
+ * output width (its rows need no alignment; 32-byte aligned ones are stored
+ * fastest); a and w 16-byte aligned, out aligned to its elements.
+ *
+ * moe_ragged_wgrad -- the weight gradient of the same product,
+ *   out[e, n, k] = sum_{r in segment e} g[r, n] a[row(r), k]    (+ out if accumulate)
+ *   g_dev        bf16 [M x ldg], N columns.
+ *   a            bf16: a_scales_dev NULL, a_dev [M x lda], row(r) = r,
+ *                a_rows_dev NULL, T ignored; or kept in 8 bits (act8_quantize):
+ *                a_dev uint8 codes [T x lda], a_scales_dev [T x ld_scales],
+ *                row(r) = a_rows[r] (int32 [M]; an index outside [0, T) adds
+ *                nothing), or r when a_rows_dev is NULL (T >= M).
+ *   out_dev      f32 or bf16 [E x N x K], contiguous; empty segments give 0.
+ *                accumulate: the sum of old value and gradient in f32, rounded
+ *                once to out's type.
+ *   workspace    moe_ragged_wgrad_workspace_size(M, N, K, E) bytes (0 unless
+ *                the result is small: segments are then split over the SMs),
+ *                16-byte aligned.
+ * Sums run in a fixed order: the same inputs give the same bits.  E <= 256,
+ * ldg % 8 == 0, lda % 8 == 0 (16 for codes), ld_scales % 4 == 0, any N and K.
+ *
+ * Both: Inf and NaN stay in the rows (WGRAD: the segments) that hold them.
+ * Timeouts as for moe_w4a4_grouped_gemm_rac (dev_status may be NULL).
+ * -------------------------------------------------------------------------- */
+NVFP4_API nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t M, const void *w_dev, int64_t N,
+                                       int64_t K, int32_t E, const int32_t *offsets_dev, int32_t transpose,
+                                       void *out_dev, int64_t ld_out, int32_t out_f32, int32_t *dev_status,
+                                       void *stream);
+
+NVFP4_API size_t moe_ragged_wgrad_workspace_size(int64_t M, int64_t N, int64_t K, int32_t E);
+
+NVFP4_API nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev, int64_t lda,
+                                        const uint8_t *a_scales_dev, int64_t ld_scales, const int32_t *a_rows_dev,
+                                        int64_t T, int64_t N, int64_t K, int32_t E, const int32_t *offsets_dev,
+                                        void *out_dev, int32_t out_f32, int32_t accumulate, void *workspace,
+                                        size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* --------------------------------------------------------------------------
+ * act8_quantize / act8_dequantize -- activations kept in 8 bits between the
+ * trainer's forward and backward pass.
+ *   codes  uint8 [M x ld_codes], E4M3 (sign in bit 7), K columns.
+ *   scales uint8 [M x ld_scales]: one byte s per 32 consecutive columns of a
+ *          row, value = e4m3(code) * 2^(s - 127).  s - 127 is the smallest
+ *          power p >= -120 with max|x| <= 448 * 2^p (s = 127 for a group of
+ *          zeros); codes = E4M3_rne(x * 2^-p).  A group that holds an Inf or
+ *          NaN gets s = 255 and codes 0x7F and reads as NaN.  Scale rows are
+ *          written up to 4 * ceil(K / 128) bytes, the padding as 127.
+ * Every kept value is exact in bf16 (|x| above 2^127 * 1.94 may round up to
+ * infinity).  Any K; ldx % 8 == 0, ld_codes % 16 == 0, ld_scales >=
+ * 4 * ceil(K / 128) and a multiple of 4; pointers 16-byte aligned (here Inf
+ * and NaN are allowed inputs).
+ *
+ * moe_swiglu_act8 -- h = bf16(silu(gate) * up) of y = [gate | up] (bf16
+ * [M x ldy], I columns each) and y kept in 8 bits, in one pass.  I % 32 == 0.
+ *
+ * moe_swiglu_act8_backward -- the SwiGLU's gradient from its kept inputs: with
+ * a, b the kept gate and up values, s = sigmoid(a), w = row_gate[r] (1 when
+ * row_gate_dev is NULL) and h = a s b,
+ *   dy[r] = [ w dh b s (1 + a (1 - s)) | w dh a s ]     bf16 [M x lddy]
+ *   gh[r] = w h                                         bf16 [M x ldgh], or NULL
+ *   dgate[r] = sum_i dh_i h_i                           f32 [M], or NULL
+ * dh_dev bf16 [M x lddh] is the gradient of the unweighted h.  f32
+ * arithmetic, one rounding; dgate in a fixed order.  I % 32 == 0; leading
+ * dimensions multiples of 8 (ld_codes 16); pointers 16-byte aligned.
+ * -------------------------------------------------------------------------- */
+NVFP4_API nvfp4_status act8_quantize(const void *x_dev, int64_t M, int64_t K, int64_t ldx, uint8_t *codes_dev,
+                                     int64_t ld_codes, uint8_t *scales_dev, int64_t ld_scales, void *stream);
+
+NVFP4_API nvfp4_status act8_dequantize(const uint8_t *codes_dev, int64_t ld_codes, const uint8_t *scales_dev,
+                                       int64_t ld_scales, int64_t M, int64_t K, void *x_dev, int64_t ldx,
+                                       void *stream);
+
+NVFP4_API nvfp4_status moe_swiglu_act8(const void *y_dev, int64_t M, int64_t I, int64_t ldy, void *h_dev, int64_t ldh,
+                                       uint8_t *codes_dev, int64_t ld_codes, uint8_t *scales_dev, int64_t ld_scales,
+                                       void *stream);
+
+NVFP4_API nvfp4_status moe_swiglu_act8_backward(const uint8_t *codes_dev, int64_t ld_codes, const uint8_t *scales_dev,
+                                                int64_t ld_scales, const void *dh_dev, int64_t lddh,
+                                                const float *row_gate_dev, int64_t M, int64_t I, void *dy_dev,
+                                                int64_t lddy, void *gh_dev, int64_t ldgh, float *dgate_dev,
+                                                void *stream);
+
+/* --------------------------------------------------------------------------
+ * moe_combine_rows -- a token's routed rows brought together again, without
+ * atomics: out[t, c] = sum_j gate[t, j] rows[dst_row[t, j], c], f32, in slot
+ * order; gate_dev NULL: unweighted.  rows bf16 [M x ld_rows], dst_row int32
+ * [T x k_r] (an index outside [0, M) adds nothing), out f32 [T x ld_out].
+ * H % 8 == 0, ld_rows % 8 == 0, ld_out % 4 == 0, 1 <= k_r <= 32.
+ *
+ * moe_route_backward -- gradient of moe_route's gates (softmax over the
+ * selected logits) with respect to the logits: with g_j = topk_gate[t, j] and
+ * d_j = dgate_row[dst_row[t, j]],
+ *   dlogits[t, topk_idx[t, j]] = g_j (d_j - sum_i g_i d_i),  0 elsewhere.
+ * dgate_row f32 [M]; dlogits f32 [T x E], written in full.
+ * -------------------------------------------------------------------------- */
+NVFP4_API nvfp4_status moe_combine_rows(const void *rows_dev, int64_t M, int64_t H, int64_t ld_rows,
+                                        const int32_t *dst_row_dev, const float *gate_dev, int64_t T, int32_t k_r,
+                                        float *out_dev, int64_t ld_out, void *stream);
+
+NVFP4_API nvfp4_status moe_route_backward(const int32_t *topk_idx_dev, const float *topk_gate_dev,
+                                          const int32_t *dst_row_dev, const float *dgate_row_dev, int64_t M, int64_t T,
+                                          int32_t E, int32_t k_r, float *dlogits_dev, void *stream);
+
+/* --------------------------------------------------------------------------
+ * moe_nvfp4_gemv -- products of a few tokens with NVFP4 weights, activations
+ * in BF16 (no activation quantization): the rollout layer's decode step.  For
+ * token t, slot j and its expert e = expert_idx[t, j],
+ *   y[t, j, n] = s_t[e] sum_k (e2m1(w) * sf)[e, n, k] x[row, k]     (f32)
+ *   MOE_EPI_STORE_F32    row = t; out f32 [T*k_r x ld_out], row t*k_r + j
+ *   MOE_EPI_SWIGLU_BF16  row = t; N = 2I; out bf16 [T*k_r x ld_out]:
+ *                        bf16(silu(y[i]) * y[I + i]), i < I
+ *   MOE_EPI_COMBINE_F32  row = t*k_r + j; out f32 [T x ld_out]:
+ *                        sum_j gate[t, j] y[t, j] in a fixed order (gate_dev
+ *                        NULL: unweighted); written, not added, no atomics
+ * expert_idx_dev int32 [T x k_r]; an index outside [0, E) gives zeros.  NULL:
+ * one dense weight (E = 1, k_r = 1), eight tokens sharing each weight read.
+ * x_dev bf16 [rows x ldx]; codes, scales, s_t as nvfp4_qdq_weights writes
+ * them for E tensors [N x K].  K % 64 == 0, any N (even for SwiGLU), ldx % 8
+ * == 0, k_r <= 32; x, codes and scales 16-byte aligned.  Any T; meant for the
+ * few tokens of a decode step (each token reads its experts' weights).
+ * -------------------------------------------------------------------------- */
+NVFP4_API nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx, const uint8_t *codes_dev,
+                                      const uint8_t *scales_dev, const float *s_t_dev, int64_t N, int64_t K,
+                                      int32_t E, const int32_t *expert_idx_dev, int32_t k_r, int32_t epilogue,
+                                      const float *gate_dev, void *out_dev, int64_t ld_out, void *stream);
 
 /* --------------------------------------------------------------------------
  * nvfp4_debug_gemm_wait_expiry -- test hook for the bounded device waits of

@@ -69,6 +69,25 @@ SIGNATURES = {
                                                           c_int32, c_int32, c_void_p, c_void_p]),
     "moe_routed_rows_bf16": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_int64,
                                        c_void_p]),
+    "moe_ragged_gemm": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_int32,
+                                  c_void_p, c_int64, c_int32, c_void_p, c_void_p]),
+    "moe_ragged_wgrad_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32]),
+    "moe_ragged_wgrad": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                   c_int64, c_int64, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_size_t,
+                                   c_void_p, c_void_p]),
+    "act8_quantize": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "act8_dequantize": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64,
+                                  c_void_p]),
+    "moe_swiglu_act8": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p,
+                                  c_int64, c_void_p]),
+    "moe_swiglu_act8_backward": (c_int32, [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
+                                           c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p]),
+    "moe_combine_rows": (c_int32, [c_void_p, c_int64, c_int64, c_int64, c_void_p, c_void_p, c_int64, c_int32, c_void_p,
+                                   c_int64, c_void_p]),
+    "moe_route_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32, c_int32,
+                                     c_void_p, c_void_p]),
+    "moe_nvfp4_gemv": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32,
+                                 c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_void_p]),
     "nvfp4_debug_gemm_wait_expiry": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                                c_int64, c_int64, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
                                                c_void_p, c_int64, c_void_p, c_int64, c_void_p]),

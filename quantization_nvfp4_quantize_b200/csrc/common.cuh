@@ -33,6 +33,12 @@ int num_sms();
 bool make_tmap_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
                   uint64_t row_bytes, uint32_t box_inner, uint32_t box_rows, CUtensorMapSwizzle swizzle);
 
+// E row-major matrices [rows x inner] (strides row_bytes and mat_bytes) with a
+// (box_inner x box_rows x 1) box; columns and rows past a matrix read as zero.
+bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint64_t inner, uint64_t rows,
+                  uint64_t mats, uint64_t row_bytes, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_rows,
+                  CUtensorMapSwizzle swizzle);
+
 #define NVFP4_REQUIRE(cond, status, ...)                 \
     do {                                                 \
         if (!(cond)) return ::nvfp4::set_error(status, __VA_ARGS__); \
@@ -53,6 +59,14 @@ __host__ __device__ __forceinline__ int64_t sf_bytes(int64_t rows, int64_t K) { 
 
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Two floats -> bf16x2, `lo` in the low half (nearest even).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 
 // Two floats -> one byte of two E2M1 codes: `lo` in bits 0..3, `hi` in 4..7.
 __device__ __forceinline__ uint32_t cvt_e2m1x2(float lo, float hi)

@@ -10,7 +10,7 @@
 //                  the routing blocks, and the expert's total.
 //   k_route_place  one CTA (32 warps) per routing block: the padded segment
 //                  starts from the totals (segments are multiples of 128 or 256
-//                  rows, the GEMM's tile height; CTA 0 also writes offsets and
+//                  rows, the GEMM's tile height, or unpadded; CTA 0 also writes offsets and
 //                  the padding rows' gates); each warp takes experts in turn
 //                  and gives every (token, slot) routed to that expert its row
 //                  = segment start + earlier blocks' count + rank in the block
@@ -285,7 +285,8 @@ extern "C" nvfp4_status moe_route(const float *logits_dev, int64_t T, int32_t E,
                   "moe_route: null pointer");
     NVFP4_REQUIRE(T >= 0 && E >= 1 && E <= MAX_EXPERTS && k_r >= 1 && k_r <= MAX_TOPK && k_r <= E,
                   NVFP4_ERR_UNSUPPORTED_SHAPE, "moe_route: need 1 <= E <= 256, 1 <= k_r <= min(8, E)");
-    NVFP4_REQUIRE(seg_align == 128 || seg_align == 256, NVFP4_ERR_INVALID_ARG, "moe_route: seg_align must be 128 or 256");
+    NVFP4_REQUIRE(seg_align == 1 || seg_align == 128 || seg_align == 256, NVFP4_ERR_INVALID_ARG,
+                  "moe_route: seg_align must be 1, 128 or 256");
     int64_t need_rows = (T * k_r + (int64_t)E * (seg_align - 1) + seg_align - 1) / seg_align * seg_align;
     NVFP4_REQUIRE(M_pad_max >= need_rows, NVFP4_ERR_INVALID_ARG,
                   "moe_route: M_pad_max must be >= %lld", (long long)need_rows);

@@ -1,0 +1,142 @@
+"""Products of a few tokens with NVFP4 weights against 64-bit products of the
+dequantized weights.  Bound: products e2m1 * sf * x are exact in f32 (at most 6
++ 8 significant bits), K additions and the final scalings err by at most 2^-23
+of sum |products| each."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from ops_util import BF16, F32, F64, I32, check, rounding, sum_bound
+from quantization_nvfp4_quantize_b200 import api
+
+pytestmark = pytest.mark.gpu
+
+
+def rnd(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(BF16)
+
+
+def weights(seed, E, N, K):
+    """NVFP4 weights from the library's quantizer and their values (64 bits)
+    through the oracle's scale layout."""
+    w = rnd(seed, E, N, K, scale=0.02)
+    w[:, 0] *= 30.0                                        # rows with other block scales
+    _, s, codes, sf = api.qdq_weights(w, want_qdq=False, want_packed=True)
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=F64, device=w.device)
+    c = codes.view(E, N, K // 2)
+    v = torch.stack([grid[(c & 15).int()], grid[(c >> 4).int()]], -1).view(E, N, K)
+    per = sf.numel() // E
+    scale = torch.stack([torch.from_numpy(oracle.unswizzle_scales(sf.view(-1)[e * per:(e + 1) * per].cpu().numpy(), N, K).copy())
+                         for e in range(E)]).to(w.device).view(torch.float8_e4m3fn).double()
+    return codes, sf, s, v * scale.repeat_interleave(16, 2) * s.double()[:, None, None]
+
+
+def bound(K, x, w):
+    return sum_bound(K + 8, torch.bmm(w.abs(), x.abs()[:, :, None])[:, :, 0])
+
+
+@pytest.mark.parametrize("T,E,kr", [(1, 8, 2), (1, 5, 1), (3, 16, 8), (9, 4, 3)])
+@pytest.mark.parametrize("N,K", [(16, 64), (130, 128), (256, 192), (1536, 2048), (34, 704)])
+def test_store_and_swiglu(cuda, T, E, kr, N, K):
+    codes, sf, s, w = weights(N + K, E, N, K)
+    x = rnd(2, T, K)
+    idx = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(t))[:kr] for t in range(T)]).to(I32).to(cuda)
+    flat = idx.view(-1).long()
+    xr = x.double().repeat_interleave(kr, 0)
+    y = torch.bmm(w[flat], xr[:, :, None])[:, :, 0]
+    b = bound(K, xr, w[flat])
+    got = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx)
+    check(got, y, b + rounding(F32, y))
+    h = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_SWIGLU_BF16)
+    a, u = y[:, : N // 2], y[:, N // 2:]
+    ba, bu = b[:, : N // 2], b[:, N // 2:]
+    sig = torch.sigmoid(a)
+    want = a * sig * u
+    # d silu / da <= 1.1; f32 sigmoid as in the SwiGLU tests
+    lim = 1.1 * ba * (u.abs() + bu) + (a * sig).abs() * bu + (16 + a.abs()) * 2.0 ** -23 * want.abs()
+    check(h, want, 1.01 * lim + rounding(BF16, want.abs() + lim))
+
+
+@pytest.mark.parametrize("T,E,kr", [(1, 8, 8), (2, 5, 1), (16, 32, 8), (5, 4, 3)])
+@pytest.mark.parametrize("N,K", [(8, 64), (130, 192), (2048, 768)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_combine(cuda, T, E, kr, N, K, gated):
+    codes, sf, s, w = weights(N + K + 1, E, N, K)
+    x = rnd(3, T * kr, K)
+    idx = torch.randint(0, E, (T, kr), generator=torch.Generator().manual_seed(4)).to(I32).to(cuda)   # repeats allowed
+    gate = torch.rand(T, kr, generator=torch.Generator().manual_seed(5)).to(cuda) if gated else None
+    flat = idx.view(-1).long()
+    c = torch.ones(T * kr, dtype=F64, device=cuda) if gate is None else gate.double().view(-1)
+    y = torch.bmm(w[flat], x.double()[:, :, None])[:, :, 0] * c[:, None]
+    b = bound(K + kr, x.double(), w[flat]) * c[:, None]
+    got = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_COMBINE_F32, gate=gate)
+    want = y.view(T, kr, N).sum(1)
+    check(got, want, b.view(T, kr, N).sum(1) + rounding(F32, want))
+    assert torch.equal(got, api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_COMBINE_F32, gate=gate))
+
+
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9, 16, 33])
+@pytest.mark.parametrize("N,K", [(1, 64), (48, 320), (640, 1024)])
+def test_dense(cuda, T, N, K):
+    codes, sf, s, w = weights(N + K + 2, 1, N, K)
+    x = rnd(6, T, K)
+    y = x.double() @ w[0].t()
+    got = api.nvfp4_gemv(x, codes, sf, s, N, K)
+    check(got, y, sum_bound(K + 8, x.double().abs() @ w[0].abs().t()) + rounding(F32, y))
+    if N % 2 == 0:
+        h = api.nvfp4_gemv(x, codes, sf, s, N, K, epilogue=api.EPI_SWIGLU_BF16)
+        idx = torch.zeros(T, 1, dtype=I32, device=cuda)
+        assert torch.equal(h, api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_SWIGLU_BF16))
+    c = api.nvfp4_gemv(x, codes, sf, s, N, K, epilogue=api.EPI_COMBINE_F32)
+    check(c, y, sum_bound(K + 8, x.double().abs() @ w[0].abs().t()) + rounding(F32, y))
+
+
+def test_every_code_and_scale_decodes_exactly(cuda):
+    """One-hot x: every E2M1 code under every E4M3 scale, exact."""
+    N, K = 128, 64
+    codes = torch.zeros(1, N, K // 2, dtype=torch.uint8, device=cuda)
+    for c in range(16):
+        codes[0, :, c // 2] |= c << (4 * (c & 1))                  # element c of block 0 holds code c
+    rows = torch.arange(N, device=cuda)
+    sfm = np.zeros((N, K // 16), np.uint8)
+    sfm[:, 0] = np.minimum(np.arange(N), 126)
+    sf = torch.from_numpy(oracle.swizzle_scales(sfm)).to(cuda).view(1, -1)
+    s = torch.ones(1, device=cuda)
+    x = torch.zeros(16, K, dtype=BF16, device=cuda)
+    x[torch.arange(16), torch.arange(16)] = 1.0
+    got = api.nvfp4_gemv(x, codes, sf, s, N, K)
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=F64, device=cuda)
+    scale = rows.clamp_max(126).to(torch.uint8).view(torch.float8_e4m3fn).double()
+    assert torch.equal(got.double(), grid[:, None] * scale[None, :])
+
+
+def test_bad_expert_gives_zeros_and_rows_keep_apart(cuda):
+    E, N, K = 3, 96, 128
+    codes, sf, s, w = weights(9, E, N, K)
+    x = rnd(10, 2, K)
+    idx = torch.tensor([[0, -1], [3, 2]], dtype=I32, device=cuda)
+    got = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx)
+    assert not bool(got[1].any()) and not bool(got[2].any()) and bool(got[0].any()) and bool(got[3].any())
+    xc = rnd(11, 4, K)
+    xc[1:3] = float("nan")                                          # rows of no expert
+    y = api.nvfp4_gemv(xc, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_COMBINE_F32)
+    assert bool(torch.isfinite(y).all())
+    x[0, 5] = float("inf")
+    got = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=torch.tensor([[0], [0]], dtype=I32, device=cuda))
+    assert bool(torch.isfinite(got[1]).all())
+    dense = api.nvfp4_gemv(x, codes[:1], sf.view(E, -1)[:1], s[:1], N, K)
+    assert bool(torch.isfinite(dense[1]).all())
+
+
+def test_strides_and_surroundings(cuda):
+    E, N, K = 2, 50, 64
+    codes, sf, s, w = weights(12, E, N, K)
+    x = rnd(13, 3, 2 * K)[:, 8:8 + K]
+    idx = torch.tensor([[0, 1], [1, 0], [1, 1]], dtype=I32, device=cuda)
+    buf = torch.full((6, N + 5), 4.0, device=cuda)
+    api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, out=buf[:, 2:2 + N])
+    assert torch.equal(buf[:, 2:2 + N], api.nvfp4_gemv(x.contiguous(), codes, sf, s, N, K, expert_idx=idx))
+    assert bool((buf[:, :2] == 4).all()) and bool((buf[:, 2 + N:] == 4).all())

@@ -1,0 +1,348 @@
+"""Grouped products over ragged segments and their gradients against 64-bit
+products: segment lengths around the tile and stage sizes, odd widths and
+strides, neighbours that hold Inf or NaN, 8-bit operands named by a row index.
+Bounds: ops_util (f32 sums of exact products, then half a step of the output
+type)."""
+import pytest
+import torch
+
+from ops_util import BF16, F32, I32, check, kept_values, offsets_of, rounding, sum_bound
+from quantization_nvfp4_quantize_b200 import api
+
+pytestmark = pytest.mark.gpu
+
+
+def rnd(seed, *shape, scale=1.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * scale).to(BF16)
+
+
+def ref_rows(a, w, off, transpose, fill):
+    """(result, sum of |products|) with rows outside the segments at `fill`."""
+    y = fill.double().clone()
+    s = torch.zeros_like(y)
+    for e in range(w.shape[0]):
+        lo, hi = int(off[e]), int(off[e + 1])
+        m = w[e].double() if transpose else w[e].double().t()
+        y[lo:hi] = a[lo:hi].double() @ m
+        s[lo:hi] = a[lo:hi].double().abs() @ m.abs()
+    return y, s
+
+
+COUNTS = [
+    [1],
+    [0, 5, 0],
+    [64, 63, 65, 1],
+    [255, 0, 256, 257, 3],
+    [1] * 17,
+    [700, 2, 0, 130],
+]
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts", COUNTS, ids=str)
+@pytest.mark.parametrize("N,K", [(8, 8), (264, 72), (520, 328), (128, 64)])
+def test_products(cuda, counts, N, K, transpose):
+    E, M = len(counts), sum(counts) + 9
+    off = offsets_of(counts, cuda, start=2)                       # rows before and behind the segments
+    w = rnd(1, E, N, K, scale=0.1)
+    a = rnd(2, M, N if transpose else K)
+    for dtype in (BF16, F32):
+        out = torch.full((M, K if transpose else N), 7.0, dtype=dtype, device=cuda)
+        got = api.ragged_gemm(a, w, off, transpose=transpose, out=out)
+        assert got.data_ptr() == out.data_ptr()
+        y, s = ref_rows(a, w, off, transpose, torch.full_like(out, 7.0))
+        check(got, y, sum_bound(a.shape[1], s) + rounding(dtype, y), f"{dtype}")
+
+
+@pytest.mark.parametrize("N", [1, 3, 33, 255, 257])
+def test_odd_output_width(cuda, N):
+    counts = [70, 0, 200]
+    off = offsets_of(counts, cuda)
+    w, a = rnd(3, 3, N, 80, scale=0.1), rnd(4, 270, 80)
+    for dtype in (BF16, F32):
+        got = api.ragged_gemm(a, w, off, out_dtype=dtype)
+        y, s = ref_rows(a, w, off, False, torch.zeros(270, N, device=cuda))
+        check(got, y, sum_bound(80, s) + rounding(dtype, y))
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_strided_operands(cuda, transpose):
+    """Rows on a longer stride; an output whose base and rows are aligned to
+    its elements only, inside a buffer that must stay as it is."""
+    counts = [100, 33, 300]
+    off = offsets_of(counts, cuda)
+    N, K = 136, 200
+    w = rnd(5, 3, N, K, scale=0.1)
+    a = rnd(6, 433, 264)[:, 8:8 + (N if transpose else K)]
+    width = K if transpose else N
+    for dtype in (BF16, F32):
+        buf = torch.full((433, width + 7), 5.0, dtype=dtype, device=cuda)
+        out = buf[:, 3:3 + width]
+        api.ragged_gemm(a, w, off, transpose=transpose, out=out)
+        y, s = ref_rows(a, w, off, transpose, torch.zeros(433, width, device=cuda))
+        check(out, y, sum_bound(a.shape[1], s) + rounding(dtype, y))
+        assert bool((buf[:, :3] == 5).all()) and bool((buf[:, 3 + width:] == 5).all())
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+def test_products_keep_bad_values_apart(cuda, transpose):
+    """Inf and NaN in another expert's rows or weights, or outside the
+    segments, reach no result."""
+    counts = [70, 60, 90]
+    off = offsets_of(counts, cuda, start=5)
+    N, K = 200, 104                                                # neither a multiple of the 64-deep stage
+    w = rnd(7, 3, N, K, scale=0.1)
+    a = rnd(8, 240, N if transpose else K)
+    w[1] = float("nan")
+    a[75:135] = float("inf")
+    a[:5] = float("nan")
+    a[225:] = float("nan")
+    got = api.ragged_gemm(a, w, off, transpose=transpose, out_dtype=F32)
+    ok = torch.cat([torch.arange(5, 75), torch.arange(135, 225)]).to(cuda)
+    y, s = ref_rows(a, w, off, transpose, torch.zeros_like(got))
+    check(got[ok], y[ok], sum_bound(a.shape[1], s[ok]) + rounding(F32, y[ok]))
+    # one bad row spoils itself only
+    a2, w2 = rnd(8, 240, a.shape[1]), rnd(7, 3, N, K, scale=0.1)
+    a2[100, 3] = float("nan")
+    got = api.ragged_gemm(a2, w2, off, transpose=transpose, out_dtype=F32)
+    assert bool(torch.isnan(got[100]).all())
+    keep = torch.ones(240, dtype=torch.bool, device=cuda)
+    keep[100], keep[:5], keep[225:] = False, False, False
+    assert bool(torch.isfinite(got[keep]).all())
+
+
+def ref_wgrad(g, a, off):
+    E = off.numel() - 1
+    y = torch.zeros(E, g.shape[1], a.shape[1], dtype=torch.float64, device=g.device)
+    s = torch.zeros_like(y)
+    for e in range(E):
+        lo, hi = int(off[e]), int(off[e + 1])
+        y[e] = g[lo:hi].double().t() @ a[lo:hi].double()
+        s[e] = g[lo:hi].double().abs().t() @ a[lo:hi].double().abs()
+    return y, s
+
+
+@pytest.mark.parametrize("counts", COUNTS, ids=str)
+@pytest.mark.parametrize("N,K", [(8, 8), (264, 72), (520, 328), (128, 257)])
+def test_weight_gradient(cuda, counts, N, K):
+    E, M = len(counts), sum(counts) + 9
+    off = offsets_of(counts, cuda, start=2)
+    g = rnd(11, M, N, scale=0.1)
+    a = rnd(12, M, -(-K // 8) * 8)[:, :K]
+    g[:2], a[:2] = float("nan"), float("inf")                      # rows of no segment
+    g[-7:], a[-7:] = float("nan"), float("inf")
+    y, s = ref_wgrad(g, a, off)
+    n = max(counts) + 1
+    for dtype in (F32, BF16):
+        got = api.ragged_wgrad(g, a, off, out_dtype=dtype)
+        check(got, y, sum_bound(n, s) + rounding(dtype, y), f"{dtype}")
+        old = rnd(13, E, N, K).to(dtype)
+        acc = old.clone()
+        api.ragged_wgrad(g, a, off, out=acc, accumulate=True)
+        z = y + old.double()
+        check(acc, z, sum_bound(n, s) + ULP_ADD * (y.abs() + old.double().abs()) + rounding(dtype, z), f"accumulate {dtype}")
+
+
+ULP_ADD = 2.0 ** -23                                               # the f32 addition of the old value
+
+
+def test_weight_gradient_keeps_bad_values_apart(cuda):
+    counts = [70, 60, 90, 0, 64]
+    off = offsets_of(counts, cuda)
+    g, a = rnd(14, 284, 264, scale=0.1), rnd(15, 284, 200)
+    g[70:130] = float("nan")
+    a[70:130] = float("inf")
+    got = api.ragged_wgrad(g, a, off)
+    y, s = ref_wgrad(g, a, off)
+    for e in (0, 2, 3, 4):
+        check(got[e], y[e], sum_bound(100, s[e]) + rounding(F32, y[e]), f"expert {e}")
+    assert bool(torch.isnan(got[1]).all())
+
+
+@pytest.mark.parametrize("E,M,N,K", [(1, 20000, 64, 96), (3, 9001, 256, 264), (2, 5000, 300, 40), (1, 600, 8, 8)])
+def test_weight_gradient_split_rows(cuda, E, M, N, K):
+    """Few output tiles: rows split over the SMs, partial sums through the
+    workspace; the same bits from run to run."""
+    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, E) > 0
+    cut = sorted([0] + [int(M * f) for f in (0.13, 0.52)][: E - 1] + [M - 3])
+    off = torch.tensor(cut, dtype=I32, device=cuda)
+    g, a = rnd(16, M, -(-N // 8) * 8, scale=0.1)[:, :N], rnd(17, M, K)
+    y, s = ref_wgrad(g, a, off)
+    old = rnd(18, E, N, K).float()
+    for dtype in (F32, BF16):
+        got = api.ragged_wgrad(g, a, off, out_dtype=dtype)
+        check(got, y, sum_bound(M, s) + rounding(dtype, y))
+        assert torch.equal(got, api.ragged_wgrad(g, a, off, out_dtype=dtype))
+        acc = old.to(dtype)
+        z = y + acc.double()
+        bound = sum_bound(M, s) + ULP_ADD * (y.abs() + acc.double().abs()) + rounding(dtype, z)
+        api.ragged_wgrad(g, a, off, out=acc, accumulate=True)
+        check(acc, z, bound)
+
+
+@pytest.mark.parametrize("counts", COUNTS[1:], ids=str)
+@pytest.mark.parametrize("N,K", [(8, 8), (264, 72), (136, 333), (520, 528)])
+def test_weight_gradient_from_kept_rows(cuda, counts, N, K):
+    """8-bit activations named by a row index: repeated rows, indices outside
+    the kept tensor, scales from the smallest to large powers."""
+    E, M, T = len(counts), sum(counts) + 4, 50
+    off = offsets_of(counts, cuda, start=1)
+    x = rnd(21, T, -(-K // 8) * 8)[:, :K].float()
+    x = (x * torch.exp2(torch.arange(T, device=cuda).float()[:, None] * 2 - 60)).to(BF16)
+    x[3] = 0
+    xk = torch.zeros(T, -(-K // 8) * 8, dtype=BF16, device=cuda)[:, :K]
+    xk.copy_(x)
+    a8 = api.act8_quantize(xk)
+    gen = torch.Generator().manual_seed(5)
+    rows = torch.randint(0, T, (M,), generator=gen).to(I32).to(cuda)
+    rows[2], rows[4] = -1, T
+    g = rnd(22, M, N, scale=0.1)
+    g[:1], g[-3:] = float("nan"), float("nan")
+    full = torch.zeros(M, K, dtype=torch.float64, device=cuda)
+    ok = (rows >= 0) & (rows < T)
+    full[ok] = kept_values(a8)[rows[ok].long()]
+    y, s = ref_wgrad(g, full, off)
+    got = api.ragged_wgrad(g, a8, off, a_rows=rows)
+    check(got, y, sum_bound(max(counts) + 1, s) + rounding(F32, y))
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_weight_gradient_many_stages_and_tiles(cuda, kept):
+    """Several tiles per SM pair, each many turns of the stage ring."""
+    counts = [4001, 0, 700, 2500, 64, 1]
+    off = offsets_of(counts, cuda)
+    M, N, K = sum(counts), 1288, 1032
+    g, x = rnd(27, M, N, scale=0.1), rnd(28, M, K)
+    a = api.act8_quantize(x) if kept else x
+    y, s = ref_wgrad(g, kept_values(a) if kept else x, off)
+    for _ in range(3):
+        check(api.ragged_wgrad(g, a, off), y, sum_bound(4001, s) + rounding(F32, y))
+
+
+def test_weight_gradient_from_kept_rows_in_order(cuda):
+    off = offsets_of([130, 3, 200], cuda)
+    a8 = api.act8_quantize(rnd(23, 333, 256))
+    g = rnd(24, 333, 264)
+    y, s = ref_wgrad(g, kept_values(a8), off)
+    check(api.ragged_wgrad(g, a8, off), y, sum_bound(200, s) + rounding(F32, y))
+
+
+def test_every_kept_code_reads_exactly(cuda):
+    """All E4M3 codes times scales from the smallest up, through the weight
+    gradient of one row with g = 1."""
+    codes = torch.arange(256, dtype=torch.uint8, device=cuda).repeat(4, 1)
+    codes[(codes & 0x7F) == 0x7F] = 0
+    scales = torch.tensor([[7] * 8, [100] * 8, [127] * 8, [240] * 8], dtype=torch.uint8, device=cuda)
+    a8 = api.Act8(codes.contiguous(), scales.contiguous())
+    off = torch.tensor([0, 1, 2, 3, 4], dtype=I32, device=cuda)
+    g = torch.ones(4, 8, dtype=BF16, device=cuda)
+    got = api.ragged_wgrad(g, a8, off)
+    want = kept_values(a8)[:, None, :].expand(4, 8, 256)
+    # products with 1 are exact in f32 down to its smallest normal
+    tiny = torch.finfo(F32).smallest_normal
+    assert bool((((got.double() - want).abs()) <= tiny * (want.abs() < tiny)).all())
+
+
+def test_kept_nan_group_reaches_the_gradient(cuda):
+    x = rnd(25, 64, 128)
+    x[10, 40] = float("inf")
+    got = api.ragged_wgrad(rnd(26, 64, 16), api.act8_quantize(x), offsets_of([64], cuda))
+    assert bool(torch.isnan(got[0, :, 32:64]).all())
+    assert bool(torch.isfinite(got[0, :, :32]).all()) and bool(torch.isfinite(got[0, :, 64:]).all())
+
+
+def test_bad_offsets_stay_inside(cuda):
+    """Descending or out-of-range bounds read as their running maximum inside
+    [0, M]."""
+    a, w, g = rnd(31, 100, 64), rnd(32, 4, 64, 64), rnd(33, 100, 64)
+    off = torch.tensor([-5, 40, 20, 500, 60], dtype=I32, device=cuda)
+    eff = torch.tensor([0, 40, 40, 100, 100], dtype=I32, device=cuda)
+    fill = torch.zeros(100, 64, dtype=F32, device=cuda)
+    assert torch.equal(api.ragged_gemm(a, w, off, out=fill.clone()), api.ragged_gemm(a, w, eff, out=fill.clone()))
+    assert torch.equal(api.ragged_wgrad(g, a, off), api.ragged_wgrad(g, a, eff))
+
+
+def test_most_experts_and_wide_tables(cuda):
+    counts = [(7 * e) % 5 for e in range(256)]
+    off = offsets_of(counts, cuda)
+    M = sum(counts)
+    a, w = rnd(34, M, 64), rnd(35, 256, 72, 64, scale=0.1)
+    got = api.ragged_gemm(a, w, off, out_dtype=F32)
+    y, s = ref_rows(a, w, off, False, torch.zeros(M, 72, device=cuda))
+    check(got, y, sum_bound(64, s) + rounding(F32, y))
+    g = rnd(36, M, 72)
+    y, s = ref_wgrad(g, a, off)
+    check(api.ragged_wgrad(g, a, off), y, sum_bound(8, s) + rounding(F32, y))
+
+
+def test_long_offsets(cuda):
+    """A row buffer whose elements pass 2^31: the last rows' products."""
+    M, K = 1_100_000, 2048
+    a = torch.empty(M, K, dtype=BF16, device=cuda)
+    tail = rnd(37, 300, K)
+    a[-300:] = tail
+    w = rnd(38, 2, 64, K, scale=0.05)
+    off = torch.tensor([M - 300, M - 100, M], dtype=I32, device=cuda)
+    out = api.ragged_gemm(a, w, off, out=torch.zeros(M, 64, dtype=F32, device=cuda))
+    small = offsets_of([200, 100], cuda)
+    y, s = ref_rows(tail, w, small, False, torch.zeros(300, 64, device=cuda))
+    check(out[-300:], y, sum_bound(K, s) + rounding(F32, y))
+    assert not bool(out[:-300].any())
+    g = torch.empty(M, 64, dtype=BF16, device=cuda)
+    g[-300:] = rnd(39, 300, 64)
+    y, s = ref_wgrad(g[-300:], tail, small)
+    check(api.ragged_wgrad(g, a, off), y, sum_bound(M, s) + rounding(F32, y))
+
+
+def test_captured_and_on_another_stream(cuda):
+    off = offsets_of([130, 70], cuda)
+    a, w, g = rnd(41, 200, 128), rnd(42, 2, 96, 128), rnd(43, 200, 96)
+    y0 = api.ragged_gemm(a, w, off)
+    d0 = api.ragged_wgrad(g, a, off)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y1 = api.ragged_gemm(a, w, off)
+        graph = torch.cuda.CUDAGraph()
+    side.synchronize()
+    with torch.cuda.graph(graph):
+        y2 = api.ragged_gemm(a, w, off)
+        d2 = api.ragged_wgrad(g, a, off)
+    y2.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y0, y1) and torch.equal(y0, y2) and torch.equal(d0, d2)
+    a.mul_(2)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y2, api.ragged_gemm(a, w, off)) and torch.equal(d2, api.ragged_wgrad(g, a, off))
+
+
+def test_gradients_match_differences(cuda):
+    """d sum(out * c) along random directions, against the gradients, by
+    central differences of the 64-bit product (linear in each factor, so the
+    difference is exact but for its own rounding)."""
+    counts = [40, 0, 25]
+    off = offsets_of(counts, cuda)
+    a, w, c = rnd(44, 65, 48), rnd(45, 3, 56, 48), rnd(46, 65, 56)
+
+    def loss(av, wv):
+        y = torch.zeros(65, 56, dtype=torch.float64, device=cuda)
+        for e in range(3):
+            lo, hi = int(off[e]), int(off[e + 1])
+            y[lo:hi] = av[lo:hi] @ wv[e].t()
+        return float((y * c.double()).sum())
+
+    da = api.ragged_gemm(c, w, off, transpose=True, out_dtype=F32).double()
+    dw = api.ragged_wgrad(c, a, off).double()
+    for seed in range(3):
+        u, v = rnd(50 + seed, 65, 48).double(), rnd(60 + seed, 3, 56, 48).double()
+        fa = (loss(a.double() + 0.5 * u, w.double()) - loss(a.double() - 0.5 * u, w.double()))
+        fw = (loss(a.double(), w.double() + 0.5 * v) - loss(a.double(), w.double() - 0.5 * v))
+        # bounds: f32 sums of 56 (65) products, weighted by |u| (|v|)
+        ba = float((sum_bound(57, (c.double().abs() @ torch.ones(56, 48, dtype=torch.float64, device=cuda)) * w.double().abs().max()) * u.abs()).sum())
+        bw = float((sum_bound(66, 65 * c.double().abs().max() * a.double().abs().max()) * v.abs()).sum())
+        assert abs(float((da * u).sum()) - fa) <= ba + 1e-6
+        assert abs(float((dw * v).sum()) - fw) <= bw + 1e-6

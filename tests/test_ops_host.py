@@ -1,0 +1,162 @@
+"""Refusals of the experts' training and decode operators: argument errors are
+returned before anything is enqueued (no GPU needed)."""
+import ctypes
+
+import pytest
+import torch
+
+from quantization_nvfp4_quantize_b200 import _lib, api
+
+FAKE = ctypes.c_void_p(0x10000)           # never dereferenced: rejected before any launch
+ODD = ctypes.c_void_p(0x10008)
+INVALID, ALIGN, SHAPE, WORKSPACE = 1, 2, 3, 6
+
+
+def calls(name, good, bad):
+    """Each (index, value, status) of `bad` put into the good arguments alone."""
+    fn = getattr(_lib.load(), name)
+    for at, value, status in bad:
+        args = list(good)
+        args[at] = value
+        assert fn(*args) == status, (name, at, value)
+
+
+def test_ragged_gemm():
+    #       a     lda  M    w     N    K   E  off  tr  out   ld  f32 stat  stream
+    good = [FAKE, 64, 100, FAKE, 128, 64, 4, FAKE, 0, FAKE, 128, 0, None, None]
+    calls("moe_ragged_gemm", good, [
+        (0, None, INVALID), (3, None, INVALID), (7, None, INVALID), (9, None, INVALID), (2, -1, INVALID),
+        (4, -1, INVALID), (6, 0, SHAPE), (6, 257, SHAPE), (2, 1 << 31, SHAPE), (4, 1 << 24, SHAPE), (5, 60, ALIGN),
+        (1, 56, ALIGN), (1, 68, ALIGN), (10, 127, ALIGN), (0, ODD, ALIGN), (3, ODD, ALIGN), (5, 0, SHAPE)])
+    lib = _lib.load()
+    back = [FAKE, 128, 100, FAKE, 128, 64, 4, FAKE, 1, FAKE, 64, 0, None, None]
+    calls("moe_ragged_gemm", back, [(1, 120, ALIGN), (10, 63, ALIGN), (4, 0, SHAPE)])
+    # nothing to do: no error, no launch
+    good[2] = 0
+    assert lib.moe_ragged_gemm(*good) == 0
+    back[5] = 0
+    back[2] = 100
+    assert lib.moe_ragged_gemm(*back) == 0
+
+
+def test_ragged_wgrad():
+    #       g     ldg  M    a     lda asc   lds rows  T   N    K   E  off   out   f32 acc ws  n  stat  stream
+    good = [FAKE, 256, 5000, FAKE, 256, None, 0, None, 0, 256, 256, 128, FAKE, FAKE, 1, 0, None, 0, None, None]
+    calls("moe_ragged_wgrad", good, [
+        (0, None, INVALID), (3, None, INVALID), (12, None, INVALID), (13, None, INVALID), (2, -1, INVALID),
+        (8, -1, INVALID), (11, 0, SHAPE), (11, 257, SHAPE), (2, 1 << 31, SHAPE), (1, 255, ALIGN), (1, 248, ALIGN),
+        (4, 248, ALIGN), (4, 260, ALIGN), (0, ODD, ALIGN), (3, ODD, ALIGN), (7, FAKE, INVALID)])
+    kept = list(good)
+    kept[5], kept[6], kept[8] = FAKE, 8, 5000
+    calls("moe_ragged_wgrad", kept, [(6, 4, ALIGN), (6, 9, ALIGN), (4, 264, ALIGN), (8, 4999, INVALID),
+                                     (5, ODD, ALIGN)])
+    # few output tiles: a workspace is required
+    lib = _lib.load()
+    few = list(good)
+    few[11] = 1
+    need = lib.moe_ragged_wgrad_workspace_size(5000, 256, 256, 1)
+    assert need > 0
+    assert lib.moe_ragged_wgrad(*few) == WORKSPACE
+    few[16], few[17] = FAKE, need - 1
+    assert lib.moe_ragged_wgrad(*few) == WORKSPACE
+    assert lib.moe_ragged_wgrad_workspace_size(5000, 4096, 4096, 1) == 0
+    assert lib.moe_ragged_wgrad_workspace_size(-1, 64, 64, 1) == 0
+    # empty results and empty sums into an accumulator
+    none = list(good)
+    none[9] = 0
+    assert lib.moe_ragged_wgrad(*none) == 0
+    none = list(good)
+    none[2], none[15] = 0, 1
+    assert lib.moe_ragged_wgrad(*none) == 0
+
+
+def test_act8():
+    good = [FAKE, 10, 100, 104, FAKE, 112, FAKE, 4, None]
+    calls("act8_quantize", good, [
+        (0, None, INVALID), (4, None, INVALID), (6, None, INVALID), (1, -1, INVALID), (2, 1 << 24, SHAPE),
+        (3, 96, ALIGN), (3, 101, ALIGN), (5, 96, ALIGN), (5, 104, ALIGN), (7, 3, ALIGN), (7, 6, ALIGN),
+        (0, ODD, ALIGN), (4, ODD, ALIGN), (6, ODD, ALIGN)])
+    good = [FAKE, 112, FAKE, 4, 10, 100, FAKE, 104, None]
+    calls("act8_dequantize", good, [
+        (0, None, INVALID), (2, None, INVALID), (6, None, INVALID), (4, -1, INVALID), (1, 96, ALIGN), (3, 3, ALIGN),
+        (7, 100, ALIGN), (0, ODD, ALIGN), (6, ODD, ALIGN)])
+    good = [FAKE, 10, 96, 192, FAKE, 96, FAKE, 192, FAKE, 8, None]
+    calls("moe_swiglu_act8", good, [
+        (0, None, INVALID), (4, None, INVALID), (6, None, INVALID), (8, None, INVALID), (2, 80, SHAPE), (1, -1, INVALID),
+        (3, 184, ALIGN), (5, 88, ALIGN), (7, 176, ALIGN), (7, 200, ALIGN), (9, 4, ALIGN), (9, 10, ALIGN),
+        (0, ODD, ALIGN)])
+    good = [FAKE, 192, FAKE, 6, FAKE, 96, None, 10, 96, FAKE, 192, None, 0, None, None]
+    calls("moe_swiglu_act8_backward", good, [
+        (0, None, INVALID), (2, None, INVALID), (4, None, INVALID), (9, None, INVALID), (8, 48, SHAPE), (1, 176, ALIGN),
+        (3, 5, ALIGN), (5, 95, ALIGN), (10, 184, ALIGN), (9, ODD, ALIGN), (11, FAKE, ALIGN)])
+    lib = _lib.load()
+    assert lib.act8_quantize(None, 0, 64, 64, None, 64, None, 4, None) == 0
+    assert lib.moe_swiglu_act8(None, 0, 32, 64, None, 32, None, 64, None, 4, None) == 0
+
+
+def test_combine_and_route_backward():
+    good = [FAKE, 10, 64, 64, FAKE, None, 5, 2, FAKE, 64, None]
+    calls("moe_combine_rows", good, [
+        (0, None, INVALID), (4, None, INVALID), (8, None, INVALID), (7, 0, INVALID), (7, 33, INVALID), (2, 60, ALIGN),
+        (3, 56, ALIGN), (9, 60, ALIGN), (9, 66, ALIGN), (0, ODD, ALIGN), (6, -1, INVALID)])
+    good = [FAKE, FAKE, FAKE, FAKE, 10, 5, 8, 2, FAKE, None]
+    calls("moe_route_backward", good, [
+        (0, None, INVALID), (1, None, INVALID), (2, None, INVALID), (3, None, INVALID), (8, None, INVALID),
+        (6, 0, SHAPE), (7, 0, SHAPE), (7, 33, SHAPE), (5, -1, INVALID)])
+
+
+def test_gemv():
+    #       x     T  ldx   codes sc    s_t   N    K    E  idx  kr epi gate  out   ld  stream
+    good = [FAKE, 2, 128, FAKE, FAKE, FAKE, 256, 128, 8, FAKE, 2, 0, None, FAKE, 256, None]
+    calls("moe_nvfp4_gemv", good, [
+        (0, None, INVALID), (3, None, INVALID), (4, None, INVALID), (5, None, INVALID), (13, None, INVALID),
+        (9, None, INVALID), (11, 2, INVALID), (11, 4, INVALID), (1, -1, INVALID), (7, 96, SHAPE), (7, 0, SHAPE),
+        (6, 0, SHAPE), (8, 0, SHAPE), (10, 0, SHAPE), (10, 33, SHAPE), (2, 120, ALIGN), (2, 132, ALIGN),
+        (14, 255, ALIGN), (0, ODD, ALIGN), (3, ODD, ALIGN), (4, ODD, ALIGN)])
+    odd = list(good)
+    odd[6], odd[11] = 257, 1
+    assert _lib.load().moe_nvfp4_gemv(*odd) == SHAPE
+    good[1] = 0
+    assert _lib.load().moe_nvfp4_gemv(*good) == 0
+
+
+def test_route_accepts_unpadded_segments():
+    lib = _lib.load()
+    # rejected for its workspace only: seg_align 1 and T * k_r rows are accepted
+    assert lib.moe_route(FAKE, 16, 8, 2, FAKE, FAKE, 1, FAKE, FAKE, FAKE, FAKE, 32, None, 0, None) == WORKSPACE
+    assert lib.moe_route(FAKE, 16, 8, 2, FAKE, FAKE, 1, FAKE, FAKE, FAKE, FAKE, 31, FAKE, 4096, None) == INVALID
+    assert lib.moe_route(FAKE, 16, 8, 2, FAKE, FAKE, 2, FAKE, FAKE, FAKE, FAKE, 64, FAKE, 4096, None) == INVALID
+
+
+def test_binding_refuses_host_tensors():
+    bf = torch.zeros(4, 64, dtype=torch.bfloat16)
+    u8 = torch.zeros(4, 64, dtype=torch.uint8)
+    off = torch.zeros(3, dtype=torch.int32)
+    a8 = api.Act8(u8, u8)
+    for call in (lambda: api.ragged_gemm(bf, bf.view(1, 4, 64), off), lambda: api.ragged_wgrad(bf, bf, off),
+                 lambda: api.act8_quantize(bf), lambda: api.act8_dequantize(a8), lambda: api.swiglu_act8(bf),
+                 lambda: api.swiglu_act8_backward(a8, bf), lambda: api.combine_rows(bf, off.view(1, 3)),
+                 lambda: api.route_backward(off.view(1, 3), off.view(1, 3).float(), off.view(1, 3), off.float(), 4),
+                 lambda: api.nvfp4_gemv(bf, u8, u8, off.float(), 4, 64)):
+        with pytest.raises(ValueError, match="CUDA tensors only"):
+            call()
+
+
+def test_binding_checks_operands():
+    dev = torch.device("cpu")
+    t = torch.zeros(4, 8)
+    with pytest.raises(ValueError, match="need torch.bfloat16"):
+        api._matrix(t, "x", torch.bfloat16, 4, 8, dev)
+    with pytest.raises(ValueError, match="need"):
+        api._matrix(t, "x", torch.float32, 4, 9, dev)
+    with pytest.raises(ValueError, match="need"):
+        api._matrix(t, "x", torch.float32, 3, 8, dev)
+    with pytest.raises(ValueError, match="contiguous"):
+        api._matrix(t.t(), "x", torch.float32, 8, 4, dev)
+    with pytest.raises(ValueError, match="expected"):
+        api._matrix(t, "x", torch.float32, 4, 8, torch.device("meta"))
+    with pytest.raises(ValueError, match="elements"):
+        api._vector(t, "x", torch.float32, 31, dev)
+    u8 = torch.zeros(4, 160, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="scales"):
+        api._act8(api.Act8(u8, u8[:, :4]), "x", 4, 160, dev)
