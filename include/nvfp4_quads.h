@@ -519,9 +519,10 @@ NVFP4_API nvfp4_status moe_w8a8_grouped_gemm(
  *   out_dev      f32 or bf16 [E x N x K], contiguous; empty segments give 0.
  *                accumulate: the sum of old value and gradient in f32, rounded
  *                once to out's type.
- *   workspace    moe_ragged_wgrad_workspace_size(M, N, K, E) bytes (0 unless
- *                the result is small: segments are then split over the SMs),
- *                16-byte aligned.
+ *   workspace    moe_ragged_wgrad_workspace_size(M, N, K, E, kept) bytes, 16-byte
+ *                aligned: kept (a in 8 bits): the kept rows in bf16, gathered
+ *                into row order; a small result: f32 partial results of
+ *                segments split over the SMs; otherwise 0.
  * Sums run in a fixed order: the same inputs give the same bits.  E <= 256,
  * ldg % 8 == 0, lda % 8 == 0 (16 for codes), ld_scales % 4 == 0, any N and K.
  *
@@ -533,7 +534,7 @@ NVFP4_API nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t M
                                        void *out_dev, int64_t ld_out, int32_t out_f32, int32_t *dev_status,
                                        void *stream);
 
-NVFP4_API size_t moe_ragged_wgrad_workspace_size(int64_t M, int64_t N, int64_t K, int32_t E);
+NVFP4_API size_t moe_ragged_wgrad_workspace_size(int64_t M, int64_t N, int64_t K, int32_t E, int32_t kept);
 
 NVFP4_API nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev, int64_t lda,
                                         const uint8_t *a_scales_dev, int64_t ld_scales, const int32_t *a_rows_dev,

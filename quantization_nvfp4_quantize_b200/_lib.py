@@ -71,7 +71,7 @@ SIGNATURES = {
                                        c_void_p]),
     "moe_ragged_gemm": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int32, c_void_p, c_int32,
                                   c_void_p, c_int64, c_int32, c_void_p, c_void_p]),
-    "moe_ragged_wgrad_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32]),
+    "moe_ragged_wgrad_workspace_size": (c_size_t, [c_int64, c_int64, c_int64, c_int32, c_int32]),
     "moe_ragged_wgrad": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64,
                                    c_int64, c_int64, c_int32, c_void_p, c_void_p, c_int32, c_int32, c_void_p, c_size_t,
                                    c_void_p, c_void_p]),

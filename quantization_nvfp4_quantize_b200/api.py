@@ -460,7 +460,7 @@ def ragged_wgrad(g: torch.Tensor, a, offsets: torch.Tensor, *, a_rows: torch.Ten
         out = torch.empty(E, N, K, dtype=out_dtype, device=dev)
     elif out.dtype not in (BF16, F32) or tuple(out.shape) != (E, N, K) or not out.is_contiguous() or out.device != dev:
         raise ValueError(f"ragged_wgrad: out must be contiguous bf16 or f32 [{E}, {N}, {K}] on g's device")
-    need = lib.moe_ragged_wgrad_workspace_size(M, N, K, E)
+    need = lib.moe_ragged_wgrad_workspace_size(M, N, K, E, kept)
     ws = torch.empty(need, dtype=U8, device=dev) if need else None
     check(lib.moe_ragged_wgrad(_p(g), _ld(g), M, _p(data), _ld(data), _p(scales), lds, _p(a_rows), T, N, K, E,
                                _p(offsets), _p(out), 1 if out.dtype is F32 else 0, 1 if accumulate else 0, _p(ws),

@@ -146,9 +146,12 @@ __device__ __forceinline__ void decode4(uint32_t w, float v[4])
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
-// One item = 16 columns, as in the quantizer.  Every kept value is exact in bf16.
+// One item = 16 columns, as in the quantizer.  Every kept value is exact in
+// bf16.  Row r of the result is kept row src_rows[r] (null: r); an index
+// outside [0, T) gives zeros.
 __global__ void __launch_bounds__(THREADS) k_act8_dequantize(const uint8_t *__restrict__ codes, int64_t ldc,
                                                              const uint8_t *__restrict__ scales, int64_t lds,
+                                                             const int32_t *__restrict__ src_rows, int64_t T,
                                                              int64_t M, int64_t K, __nv_bfloat16 *__restrict__ x,
                                                              int64_t ldx, int items)
 {
@@ -160,14 +163,20 @@ __global__ void __launch_bounds__(THREADS) k_act8_dequantize(const uint8_t *__re
     const int ditem = (int)(stride - drow * items);
     while (row < M) {
         const int64_t c = (int64_t)item * 16;
-        const float s = scale_of(scales[row * lds + (item >> 1)]);
-        const uint8_t *src = codes + row * ldc + c;
+        const int64_t from = src_rows ? (int64_t)src_rows[row] : row;
+        float s = 1.0f;
         uint32_t w[4] = {0, 0, 0, 0};
-        if (c + 16 <= K) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(src);
-            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-        } else {
-            for (int i = 0; c + i < K; ++i) w[i >> 2] |= (uint32_t)src[i] << (8 * (i & 3));
+        if (from >= 0 && from < T) {
+            s = scale_of(scales[from * lds + (item >> 1)]);
+            const uint8_t *src = codes + from * ldc + c;
+            if (c + 16 <= K) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(src);
+                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < K) w[i >> 2] |= (uint32_t)src[i] << (8 * (i & 3));
+            }
         }
         uint32_t o[8];
 #pragma unroll
@@ -182,8 +191,9 @@ __global__ void __launch_bounds__(THREADS) k_act8_dequantize(const uint8_t *__re
             *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4 *>(dst + 8) = make_uint4(o[4], o[5], o[6], o[7]);
         } else {
-            for (int i = 0; c + i < K; ++i)
-                dst[i] = __ushort_as_bfloat16((unsigned short)(o[i >> 1] >> (16 * (i & 1))));
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < K) dst[i] = __ushort_as_bfloat16((unsigned short)(o[i >> 1] >> (16 * (i & 1))));
         }
         row += drow;
         item += ditem;
@@ -374,6 +384,16 @@ static unsigned stream_blocks(int64_t work)
 }
 
 }  // namespace act8
+
+nvfp4_status act8_expand(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, const int32_t *rows,
+                         int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, cudaStream_t stream)
+{
+    const int items = (int)((K + 15) / 16);
+    act8::k_act8_dequantize<<<act8::stream_blocks(M * items), act8::THREADS, 0, stream>>>(
+        codes, ldc, scales, lds, rows, T, M, K, reinterpret_cast<__nv_bfloat16 *>(x), ldx, items);
+    return check_launch("k_act8_dequantize");
+}
+
 }  // namespace nvfp4
 
 using namespace nvfp4;
@@ -415,10 +435,7 @@ extern "C" nvfp4_status act8_dequantize(const uint8_t *codes_dev, int64_t ld_cod
     NVFP4_REQUIRE(ld_scales >= (K + 31) / 32, NVFP4_ERR_ALIGNMENT, "act8_dequantize: ld_scales must be >= ceil(K / 32)");
     NVFP4_REQUIRE(aligned16(x_dev) && aligned16(codes_dev), NVFP4_ERR_ALIGNMENT,
                   "act8_dequantize: pointers must be 16-byte aligned");
-    const int items = (int)((K + 15) / 16);
-    k_act8_dequantize<<<stream_blocks(M * items), THREADS, 0, (cudaStream_t)stream>>>(
-        codes_dev, ld_codes, scales_dev, ld_scales, M, K, reinterpret_cast<__nv_bfloat16 *>(x_dev), ldx, items);
-    return check_launch("k_act8_dequantize");
+    return act8_expand(codes_dev, ld_codes, scales_dev, ld_scales, nullptr, M, M, K, x_dev, ldx, (cudaStream_t)stream);
 }
 
 extern "C" nvfp4_status moe_swiglu_act8(const void *y_dev, int64_t M, int64_t I, int64_t ldy, void *h_dev, int64_t ldh,

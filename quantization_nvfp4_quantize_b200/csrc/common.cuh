@@ -39,6 +39,12 @@ bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint
                   uint64_t mats, uint64_t row_bytes, uint64_t mat_bytes, uint32_t box_inner, uint32_t box_rows,
                   CUtensorMapSwizzle swizzle);
 
+// Rows of an 8-bit kept tensor (codes [T x ldc], scales [T x lds]) as bf16
+// [M x ldx]: row r is kept row rows[r] (null: r), zeros for an index outside
+// [0, T).  Arguments as act8_dequantize checks them.
+nvfp4_status act8_expand(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, const int32_t *rows,
+                         int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, cudaStream_t stream);
+
 #define NVFP4_REQUIRE(cond, status, ...)                 \
     do {                                                 \
         if (!(cond)) return ::nvfp4::set_error(status, __VA_ARGS__); \

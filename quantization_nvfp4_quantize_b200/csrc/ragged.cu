@@ -6,46 +6,61 @@
 //   FWD    out[r, n]  = sum_k a[r, k] w_e[n, k]
 //   DGRAD  out[r, k]  = sum_n g[r, n] w_e[n, k]
 //   WGRAD  dw_e[n, k] = sum_{r in e} g[r, n] a[r, k]
-//   KEPT   WGRAD with a kept in 8 bits (E4M3, one power-of-two scale per 32
-//          columns of a row) and named by a row index
 //
 // Bound by the tensor pipe for segments of a few hundred rows and more, by the
-// weights' bytes below that (WGRAD: by the f32 result's bytes).
+// weights' bytes below that (WGRAD: by the result's bytes).
 //
-// A cluster of two CTAs computes 256 x 256 tiles with tcgen05 .cta_group::2:
-// each CTA stages 128 rows of the M-side operand and 128 of the N-side one,
-// 64 deep, 32 KB a stage, in a ring of stages; the even CTA issues the MMAs.
+// A cluster of two CTAs computes one tile with tcgen05 .cta_group::2: each CTA
+// stages half of the M-side operand (128 of 256) and half of the N-side one
+// (up to 128), 64 deep, in a ring of stages; the even CTA issues the MMAs.
 // TMEM holds two 256-column accumulators, so one tile's epilogue runs under
 // the next tile's MMAs.
 //
+// Which operand goes where: the M side of an MMA has 256 rows whatever the
+// tile needs, the N side any multiple of 64 up to 256.  FWD and DGRAD
+// therefore put the weights on the M side and the ragged rows on the N side: a
+// segment is cut into equal tiles of at most 256 rows, rounded up to 64, and
+// neither MMAs nor loads are spent on the rest.
+// (The rows on the M side pay for half-empty last tiles.)
+//
 // The tensor core takes an operand either way round (instruction descriptor
 // bits 15 / 16), so no operand is ever transposed in memory:
-//   K-major    the reduction runs along a row: a 128-row x 64-column TMA box;
-//   MN-major   the reduction runs down the rows: two 64-column x 64-row boxes.
-// FWD is K x K, DGRAD K x MN, WGRAD MN x MN.
+//   K-major    the reduction runs along a row: row boxes of 64 columns;
+//   MN-major   the reduction runs down the rows: 64-column x 64-row boxes.
+// FWD is K x K, DGRAD MN x K, WGRAD MN x MN.
+// The M side is always the output's contiguous dimension: TMEM lanes are then
+// neighbouring columns of one output row, and a warp's store covers a 128-byte
+// line.  (WGRAD with one row per lane, 32 lines per store: 528 us at 1536 x
+// 2048, 128 experts; the stores held up the barrier traffic of the other warps.)
 //
 // Ragged reduction (WGRAD): a segment's last stage also holds rows of the next
 // expert, or rows nobody wrote.  Zeroing one operand would not do (0 * NaN), so
 // that stage lands on a barrier of its own CTA, warp 3 zeroes the surplus rows
 // of both operands in shared memory and only then reports the stage to the
 // MMA issuer.  Ragged rows (FWD, DGRAD) need nothing: a surplus row only makes
-// an accumulator row that the epilogue does not store.
+// an accumulator column that the epilogue does not store.
 //
-// KEPT: one converter warp per slot of the stage ring: 64 rows x 128 columns of
-// codes from global memory to registers (before the slot is free), to BF16
-// (exact), to the slot in the MMA's swizzle.  Not more warps than slots: a
-// warp further ahead could find its slot two uses behind, where the parity of
-// the slot's barrier looks like a free one.  The codes are read at their own size
-// and never expanded in global memory.
+// Long sums (WGRAD): the tensor core's f32 accumulation truncates, an error
+// that grows with the number of additions (1.6e-6 in norm after 1024 rows,
+// 2.8e-7 for f32 additions rounded to nearest).  The accumulator is therefore
+// handed over after at most CHUNK stages and the chunks are added in the epilogue's
+// registers.
+//
+// Rows kept in 8 bits (E4M3, a power-of-two scale per 32 columns) are first
+// expanded, gathered by their row index, into a BF16 copy in the workspace
+// (exact).  Converting inside the WGRAD kernel was built and measured: every
+// M-side tile converts its rows again, and 6 converter warps could not keep up
+// (1536 x 2048, 128 experts, 32768 rows: 731 us against 471 us for a BF16
+// operand).
 //
 // WGRAD with few output tiles splits every segment's rows over several tiles:
 // f32 partial results in the workspace, added in split order by a second
 // kernel (no atomics: the result does not change from run to run).
 //
-// Warps: 0, 2 TMA producers; 1 MMA issuer; 3 the surplus-row fixer; 4..11
-// epilogue; 12..17 converters (KEPT).  Every mbarrier wait is bounded (1 s);
-// on expiry the kernel records NVFP4_ERR_TIMEOUT, its roles stop, copies in
-// flight get 1 ms to land, MMAs are drained and TMEM is freed.
+// Warps: 0, 2 TMA producers (M side, N side); 1 MMA issuer; 3 the surplus-row
+// fixer; 4..11 epilogue.  Every mbarrier wait is bounded (1 s); on expiry the
+// kernel records NVFP4_ERR_TIMEOUT, its roles stop, copies in flight get 1 ms
+// to land, MMAs are drained and TMEM is freed.
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -56,53 +71,38 @@
 namespace nvfp4 {
 namespace ragged {
 
-constexpr int TILE = 256;                        // both output dimensions of a pair's tile
+constexpr int TILE = 256;                        // M side of a pair's tile, most of its N side
+constexpr int N_STEP = 64;                       // granularity of the N side
 constexpr int BK = 64;                           // reduction depth of a stage
+constexpr int CHUNK = 8;                         // WGRAD: most stages summed in one accumulator
 constexpr int STAGES = 6;
 constexpr uint32_t OPER_BYTES = 128 * BK * 2;    // one operand of one CTA: 16 KB
 constexpr uint32_t BOX_BYTES = 64 * BK * 2;      // one MN-major box: 8 KB
+constexpr int ROW_BOX = 32;                      // rows per box of the ragged rows (FWD, DGRAD)
 constexpr uint32_t STAGE_BYTES = 2 * OPER_BYTES;
 constexpr uint32_t SMEM = STAGES * STAGE_BYTES + 1024 /*align*/ + 4096 /*barriers, offsets*/;
 static_assert(SMEM <= 232448, "shared memory budget");
-constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, CONV_WARP0 = 12, CONV_WARPS = STAGES;
-constexpr int PROD_A_WARP = 0, MMA_WARP = 1, PROD_B_WARP = 2, FIX_WARP = 3;
+constexpr int EPI_WARPS = 8, EPI_WARP0 = 4;
+constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+constexpr int PROD_M_WARP = 0, MMA_WARP = 1, PROD_N_WARP = 2, FIX_WARP = 3;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_E = 256;
 constexpr uint64_t TIMEOUT_NS = 1000000000ull;
 
-enum Mode { FWD = 0, DGRAD = 1, WGRAD = 2, KEPT = 3 };
-
-template <int MODE>
-struct Cfg {
-    static constexpr bool RAGGED_K = MODE == WGRAD || MODE == KEPT;
-    static constexpr bool A_MN = RAGGED_K;                   // M-side operand MN-major
-    static constexpr bool B_MN = MODE != FWD;                // N-side operand MN-major
-    static constexpr int THREADS = MODE == KEPT ? 384 + 32 * CONV_WARPS : 384;
-    // arrivals per stage: both producers; KEPT: the producer's two, one converter warp per CTA
-    static constexpr uint32_t FULL_COUNT = MODE == KEPT ? 4 : 2;
-};
+enum Mode { FWD = 0, DGRAD = 1, WGRAD = 2 };
 
 struct Params {
     int64_t M;                 // rows of the routed order
-    int64_t out_m, out_n;      // WGRAD: N x K of one expert's gradient; else out_n = output columns
-    int64_t red;               // reduction length (FWD: K, DGRAD: N)
+    int64_t out_m, out_n;      // M-side extent (FWD: N, DGRAD, WGRAD: K); WGRAD: N-side extent (N)
+    int64_t red;               // FWD, DGRAD: reduction length
     int E;
-    int n_tiles;               // tiles along the N side
-    int m_tiles;               // WGRAD: tiles along the M side
+    int m_tiles;               // tiles along the M side
+    int n_tiles;               // WGRAD: tiles along the N side
     int splits;                // WGRAD: row splits of every segment
     const int32_t *offsets;
     void *out;
     int64_t ld_out;
-    int out_f32;
-    int accumulate;            // WGRAD: add to out
-    int vec_bytes;             // widest store that out's base and rows allow: 32, 16 or 0 (element by element)
-    // KEPT
-    const uint8_t *codes;
-    int64_t ld_codes;
-    const uint8_t *scales;
-    int64_t ld_scales;
-    const int32_t *a_rows;     // or null: row r itself
-    int64_t T;                 // kept rows
+    int pairs;                 // bf16 out: two neighbouring columns may be stored at once
     int32_t *dev_status;
 };
 
@@ -119,49 +119,57 @@ struct Shared {
     int tiles[MAX_E + 1];      // FWD / DGRAD: row tiles before expert e
 };
 
+// A converged warp's wait, bounded: false on a timeout or another role's.
+// `cluster`: the peer CTA's threads wrote shared memory before they arrived.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *dev_status,
-                                         bool ignore_abort = false)
+                                         bool ignore_abort = false, bool cluster = false)
 {
+    bool ok = true;
     uint64_t t0 = 0;
-    for (uint32_t i = 0;; ++i) {
-        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-        if ((i & 63u) == 63u) {
-            if (!ignore_abort && *abort_flag) return false;
+    for (uint32_t i = 1;; ++i) {
+        if (cluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait_hint(bar, parity)) break;
+        if ((i & 15u) == 0u) {
+            if (!ignore_abort && *abort_flag) { ok = false; break; }
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
             else if (now - t0 > TIMEOUT_NS) {
                 *abort_flag = 1;
                 report_status(dev_status, NVFP4_ERR_TIMEOUT);
-                return false;
+                ok = false;
+                break;
             }
         }
     }
+    return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;         // a uniform answer
 }
 
 // What a tile covers.
 struct Tile {
     int e;
-    int64_t m0, m_end;         // M-side start and end (rows, or rows of w for WGRAD)
-    int64_t n0;
+    int64_t m0;                // M-side start
+    int64_t n0, n_end;         // N-side start and end
+    int nt;                    // N-side size of the MMA
     int r0, r1;                // WGRAD: its rows
     int stages;                // reduction stages (0: WGRAD of an empty segment)
+    int chunk;                 // stages per accumulator
     int split;
 };
 
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(const Params &p, const Shared *sh, int64_t t)
+__device__ __forceinline__ Tile tile_of(const Params &p, const Shared *sh, int t)
 {
     Tile w;
-    if (Cfg<MODE>::RAGGED_K) {
+    if (MODE == WGRAD) {
         const int per = p.m_tiles * p.n_tiles * p.splits;
-        w.e = (int)(t / per);
-        int rem = (int)(t - (int64_t)w.e * per);
+        w.e = t / per;
+        int rem = t - w.e * per;
         w.split = rem / (p.m_tiles * p.n_tiles);
         rem -= w.split * (p.m_tiles * p.n_tiles);
         const int mt = rem / p.n_tiles;
         w.m0 = (int64_t)mt * TILE;
-        w.m_end = p.out_m;
         w.n0 = (int64_t)(rem - mt * p.n_tiles) * TILE;
+        w.n_end = p.out_n;
+        w.nt = TILE;
         const int lo = sh->off[w.e], hi = sh->off[w.e + 1];
         // whole stages per split, so that only a segment's last stage is ragged
         const int chunk = ((hi - lo + p.splits - 1) / p.splits + BK - 1) / BK * BK;
@@ -169,73 +177,128 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Shared *sh, int64
         w.r0 = (int)min((int64_t)hi, r0);
         w.r1 = (int)min((int64_t)hi, r0 + chunk);
         w.stages = (w.r1 - w.r0 + BK - 1) / BK;
+        const int chunks = max(1, (w.stages + CHUNK - 1) / CHUNK);
+        w.chunk = max(1, (w.stages + chunks - 1) / chunks);
     } else {
-        const int rt = (int)(t / p.n_tiles);
+        const int rt = t / p.m_tiles;
         int lo = 0, hi = p.E;                        // tiles[lo] <= rt < tiles[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (sh->tiles[mid] <= rt) lo = mid; else hi = mid;
         }
+        // an expert's tiles: its row tiles innermost, they share a weight tile
+        const int row_tiles = sh->tiles[lo + 1] - sh->tiles[lo];
+        const int idx = t - sh->tiles[lo] * p.m_tiles;
+        const int mt = idx / row_tiles, i = idx - mt * row_tiles;
+        const int len = sh->off[lo + 1] - sh->off[lo];
+        const int size = ((len + row_tiles - 1) / row_tiles + N_STEP - 1) / N_STEP * N_STEP;
         w.e = lo;
-        w.m0 = (int64_t)sh->off[lo] + (int64_t)(rt - sh->tiles[lo]) * TILE;
-        w.m_end = sh->off[lo + 1];
-        w.n0 = (t - (int64_t)rt * p.n_tiles) * TILE;
+        w.m0 = (int64_t)mt * TILE;
+        w.n0 = (int64_t)sh->off[lo] + (int64_t)i * size;
+        w.n_end = sh->off[lo + 1];
+        w.nt = min(size, (int)((w.n_end - w.n0 + N_STEP - 1) / N_STEP) * N_STEP);
         w.r0 = w.r1 = 0;
         w.split = 0;
-        w.stages = (int)((p.red + BK - 1) / BK);
+        w.stages = w.chunk = (int)((p.red + BK - 1) / BK);
     }
     return w;
 }
 
-// E4M3 pair codes -> two BF16 values times a scale pair: the code's exponent
-// and mantissa bits read as value * 2^-120 in a BF16, its zero exponent
-// (subnormals) included; both multiplications are exact.
-__device__ __forceinline__ uint32_t kept_pair(uint32_t t, uint32_t scale2)
+// tile_of with every field broadcast, so that the compiler knows it to be the
+// same in all lanes.
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(const Params &p, const Shared *sh, int t)
 {
-    const uint32_t v = ((t >> 4) & 0x07F007F0u) | (t & 0x80008000u);
-    const uint32_t up = 0x7B807B80u;                 // 2^120
-    __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&v), *reinterpret_cast<const __nv_bfloat162 *>(&up));
-    r = __hmul2(r, *reinterpret_cast<const __nv_bfloat162 *>(&scale2));
-    return *reinterpret_cast<const uint32_t *>(&r);
+    Tile w = tile_of<MODE>(p, sh, t);
+    w.e = __shfl_sync(0xffffffffu, w.e, 0);
+    w.m0 = __shfl_sync(0xffffffffu, w.m0, 0);
+    w.n0 = __shfl_sync(0xffffffffu, w.n0, 0);
+    w.n_end = __shfl_sync(0xffffffffu, w.n_end, 0);
+    w.nt = __shfl_sync(0xffffffffu, w.nt, 0);
+    w.r0 = __shfl_sync(0xffffffffu, w.r0, 0);
+    w.r1 = __shfl_sync(0xffffffffu, w.r1, 0);
+    w.stages = __shfl_sync(0xffffffffu, w.stages, 0);
+    w.chunk = __shfl_sync(0xffffffffu, w.chunk, 0);
+    w.split = __shfl_sync(0xffffffffu, w.split, 0);
+    return w;
 }
 
-// 2^(s - 127) in both halves; NaN for s = 255.
-__device__ __forceinline__ uint32_t kept_scale(uint32_t s)
+// WGRAD's epilogue holds 128 sums and 32 columns in flight per thread: the
+// control warps pass registers on (56 + 2 x 224 of the 3 x 168 per warpgroup
+// that the block starts with).
+template <int MODE>
+__device__ __forceinline__ void give_registers()
 {
-    return s == 255u ? 0x7FC07FC0u : s == 0u ? 0x00400040u : s * 0x00800080u;
-}
-
-// 16 codes of which `left` are inside the row.
-__device__ __forceinline__ uint4 load_codes(const uint8_t *src, int64_t left)
-{
-    if (left >= 16) return __ldg(reinterpret_cast<const uint4 *>(src));
-    uint32_t w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 15; ++i)
-        if (i < left) w[i >> 2] |= (uint32_t)src[i] << (8 * (i & 3));
-    return make_uint4(w[0], w[1], w[2], w[3]);
+    if (MODE == WGRAD) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(Cfg<MODE>::THREADS, 1)
-k_ragged_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b, const Params p)
+__device__ __forceinline__ void take_registers()
 {
-    using C = Cfg<MODE>;
+    if (MODE == WGRAD) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+}
+
+// 32 output rows from `row`, of which `rows` exist, at column m = this lane's.
+// ADD: to the old value, in f32.
+template <bool ADD>
+__device__ __forceinline__ void store_rows(const Params &p, float *out, int64_t row, int rows, int64_t m,
+                                           const float (&v)[32])
+{
+    float *dst = out + row * p.ld_out + m;
+    if (m >= p.out_m) rows = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j, dst += p.ld_out)
+        if (j < rows) *dst = ADD ? *dst + v[j] : v[j];
+}
+
+// The same as bf16.  Neighbouring lanes exchange values: the even lane stores
+// row j, the odd lane row j + 1, both of columns m & ~1 and m | 1, so a store
+// instruction writes 2 rows x 64 bytes.
+template <bool ADD>
+__device__ __forceinline__ void store_rows(const Params &p, __nv_bfloat16 *out, int64_t row, int rows, int64_t m,
+                                           const float (&v)[32])
+{
+    const int odd = (int)(threadIdx.x & 1);
+    const int64_t me = m - odd;
+    __nv_bfloat16 *dst = out + (row + odd) * p.ld_out + me;
+    const bool has_lo = me < p.out_m, has_hi = me + 1 < p.out_m;
+    const bool pair = p.pairs != 0 && has_hi;
+    rows -= odd;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2, dst += 2 * p.ld_out) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+        float lo = odd ? got : v[j], hi = odd ? v[j + 1] : got;
+        if (ADD) {
+            if (j < rows && has_lo) lo += __bfloat162float(dst[0]);
+            if (j < rows && has_hi) hi += __bfloat162float(dst[1]);
+        }
+        const uint32_t b = pack_bf16(lo, hi);
+        if (j < rows && pair) *reinterpret_cast<uint32_t *>(dst) = b;
+        if (j < rows && !pair && has_lo) dst[0] = __ushort_as_bfloat16((unsigned short)b);
+        if (j < rows && !pair && has_hi) dst[1] = __ushort_as_bfloat16((unsigned short)(b >> 16));
+    }
+}
+
+template <int MODE, typename OutT, bool ADD>
+__global__ void __launch_bounds__(THREADS, 1)
+k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_n, const Params p)
+{
+    constexpr bool A_MN = MODE != FWD, B_MN = MODE == WGRAD;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *stage_base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     Shared *sh = reinterpret_cast<Shared *>(stage_base + STAGES * STAGE_BYTES);
     volatile int *abort_flag = &sh->abort_flag;
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t rank = ptx::cluster_ctarank();
     const bool leader = rank == 0;
     const int unit = (int)(blockIdx.x >> 1), n_units = (int)(gridDim.x >> 1);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            ptx::mbar_init(ptx::smem_u32(&sh->full[s]), C::FULL_COUNT);
+            ptx::mbar_init(ptx::smem_u32(&sh->full[s]), 2);
             ptx::mbar_init(ptx::smem_u32(&sh->empty[s]), 1);
-            ptx::mbar_init(ptx::smem_u32(&sh->raw[s]), MODE == KEPT ? 1 : 2);
+            ptx::mbar_init(ptx::smem_u32(&sh->raw[s]), 2);
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(ptx::smem_u32(&sh->tmem_full[i]), 1);
@@ -303,58 +366,66 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
     ptx::tc_fence_before();
     ptx::cluster_sync();                   // barriers of both CTAs initialized before any remote use
     ptx::tc_fence_after();
-    const uint32_t tmem = sh->tmem_base;
-    const int64_t total = C::RAGGED_K ? (int64_t)p.E * p.m_tiles * p.n_tiles * p.splits
-                                      : (int64_t)sh->tiles[p.E] * p.n_tiles;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
+    const int total = MODE == WGRAD ? p.E * p.m_tiles * p.n_tiles * p.splits : sh->tiles[p.E] * p.m_tiles;
 
-    if (warp == PROD_A_WARP || (warp == PROD_B_WARP && MODE != KEPT)) {
-        if (lane == 0) {
-            // ------------------------------------------------- producers
-            const bool role_a = warp == PROD_A_WARP;
-            const CUtensorMap *tm = role_a ? &tm_a : &tm_b;
-            ptx::prefetch_tmap(tm);
+    if (warp == PROD_M_WARP || warp == PROD_N_WARP) {
+        give_registers<MODE>();
+        // ----------------------------------------------------- producers
+        // The whole warp runs the loop and one elected lane issues: loop state
+        // and copy operands then live in uniform registers.  (Issued from a
+        // lane == 0 branch, each TMA copy cost ~110 and each MMA ~125 cycles of
+        // its thread.)
+        {
+            const bool one = ptx::elect_one();
+            const bool m_side = warp == PROD_M_WARP;
+            const CUtensorMap *tm = m_side ? &tm_m : &tm_n;
+            if (one) ptx::prefetch_tmap(tm);
             uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int64_t t = unit; ok && t < total; t += n_units) {
+            for (int t = unit; ok && t < total; t += n_units) {
                 const Tile w = tile_at<MODE>(p, sh, t);
-                // this CTA's 128 of the tile's 256 rows / columns
-                const int mn = (int)((role_a ? w.m0 : w.n0) + rank * 128);
+                // this CTA's half of the operand
+                const int half_n = w.nt / 2;
+                const int mn = (int)(m_side ? w.m0 + rank * 128 : w.n0 + (int)rank * half_n);
+                                const uint32_t bytes = m_side || MODE == WGRAD ? OPER_BYTES : (uint32_t)half_n * (BK * 2);
                 for (int kb = 0; kb < w.stages; ++kb) {
                     if (!wait_bar(ptx::smem_u32(&sh->empty[stage]), phase ^ 1u, abort_flag, p.dev_status)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = ptx::smem_u32(stage_base + stage * STAGE_BYTES + (role_a ? 0 : OPER_BYTES));
+                    const uint32_t dst = ptx::smem_u32(stage_base + stage * STAGE_BYTES + (m_side ? 0 : OPER_BYTES));
                     const uint32_t fb = ptx::smem_u32(&sh->full[stage]);
-                    if (C::RAGGED_K) {
-                        const int row = w.r0 + kb * BK;
-                        if (row + BK > w.r1) {
-                            // ragged: land in this CTA, the fixer reports it
-                            const uint32_t rb = ptx::smem_u32(&sh->raw[stage]);
+                    const uint32_t lfb = ptx::mapa_shared(fb, 0);      // the leader's barrier
+                    const int row = w.r0 + kb * BK;
+                    if (MODE == WGRAD && row + BK > w.r1) {
+                        // ragged: land in this CTA, the fixer reports it
+                        const uint32_t rb = ptx::smem_u32(&sh->raw[stage]);
+                        if (one) {
                             ptx::mbar_arrive_expect_tx(rb, OPER_BYTES);
                             ptx::tma_load_2d(dst, tm, mn, row, rb);
                             ptx::tma_load_2d(dst + BOX_BYTES, tm, mn + 64, row, rb);
-                        } else {
-                            const uint32_t lfb = ptx::mapa_shared(fb, 0);
-                            if (leader) {
-                                ptx::mbar_arrive_expect_tx(fb, 2 * OPER_BYTES);
-                                if (MODE == KEPT) ptx::mbar_arrive(fb);
-                            }
-                            ptx::tma_load_2d_pair(dst, tm, mn, row, lfb);
-                            ptx::tma_load_2d_pair(dst + BOX_BYTES, tm, mn + 64, row, lfb);
                         }
                     } else {
-                        const uint32_t lfb = ptx::mapa_shared(fb, 0);
-                        if (leader) ptx::mbar_arrive_expect_tx(fb, 2 * OPER_BYTES);
-                        if (role_a) {
-                            ptx::tma_load_2d_pair(dst, tm, kb * BK, mn, lfb);
-                        } else if (C::B_MN) {
-                            ptx::tma_load_3d_pair(dst, tm, mn, kb * BK, w.e, lfb);
-                            ptx::tma_load_3d_pair(dst + BOX_BYTES, tm, mn + 64, kb * BK, w.e, lfb);
+                        if (one && leader) ptx::mbar_arrive_expect_tx(fb, 2 * bytes);
+                        if (MODE == WGRAD) {
+                            if (one) {
+                                ptx::tma_load_2d_pair(dst, tm, mn, row, lfb);
+                                ptx::tma_load_2d_pair(dst + BOX_BYTES, tm, mn + 64, row, lfb);
+                            }
+                        } else if (!m_side) {
+                            for (int i = 0; i < half_n; i += ROW_BOX)
+                                if (one) ptx::tma_load_2d_pair(dst + i * (BK * 2), tm, kb * BK, mn + i, lfb);
+                        } else if (MODE == DGRAD) {
+                            if (one) {
+                                ptx::tma_load_3d_pair(dst, tm, mn, kb * BK, w.e, lfb);
+                                ptx::tma_load_3d_pair(dst + BOX_BYTES, tm, mn + 64, kb * BK, w.e, lfb);
+                            }
                         } else {
-                            ptx::tma_load_3d_pair(dst, tm, kb * BK, mn, w.e, lfb);
+                            if (one) ptx::tma_load_3d_pair(dst, tm, kb * BK, mn, w.e, lfb);
                         }
                     }
+                    __syncwarp();
                     if (++stage == STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -366,80 +437,92 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
         }
         __syncwarp();
     } else if (warp == MMA_WARP) {
-        if (lane == 0 && leader) {
+        give_registers<MODE>();
+        if (leader) {
             // ----------------------------------------------- MMA issuer
-            const uint32_t idesc = ptx::idesc_bf16(TILE, TILE) | (C::A_MN ? 1u << 15 : 0u) | (C::B_MN ? 1u << 16 : 0u);
+            const bool one = ptx::elect_one();
             uint32_t stage = 0, phase = 0;
-            bool ok = true, issued = false;
-            int iter = 0;
-            for (int64_t t = unit; ok && t < total; t += n_units) {
+            bool ok = true, issued = false, ready = false;
+            const uint32_t full0 = ptx::smem_u32(&sh->full[0]), empty0 = ptx::smem_u32(&sh->empty[0]);
+            const uint32_t s0 = ptx::smem_u32(stage_base);
+            const uint64_t a_desc = A_MN ? ptx::make_sdesc(s0, BOX_BYTES, 1024, 2) : ptx::make_sdesc(s0, 16, 1024, 2);
+            const uint64_t b_desc = B_MN ? ptx::make_sdesc(s0 + OPER_BYTES, BOX_BYTES, 1024, 2)
+                                         : ptx::make_sdesc(s0 + OPER_BYTES, 16, 1024, 2);
+            int iter = 0;                                // accumulators handed over
+            for (int t = unit; ok && t < total; t += n_units) {
                 const Tile w = tile_at<MODE>(p, sh, t);
-                if (w.stages == 0) continue;
-                const int acc = iter & 1;
-                if (!wait_bar(ptx::smem_u32(&sh->tmem_empty[acc]), (uint32_t)((iter >> 1) & 1) ^ 1u, abort_flag,
-                              p.dev_status)) {
-                    ok = false;
-                    break;
-                }
-                ++iter;
-                ptx::tc_fence_after();
-                const uint32_t d = tmem + (uint32_t)acc * TILE;
-                const int64_t len = C::RAGGED_K ? (int64_t)(w.r1 - w.r0) : p.red;
-                for (int kb = 0; kb < w.stages; ++kb) {
-                    if (!wait_bar(ptx::smem_u32(&sh->full[stage]), phase, abort_flag, p.dev_status)) {
+                const uint32_t idesc = ptx::idesc_bf16(TILE, (uint32_t)w.nt) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+                const int64_t len = MODE == WGRAD ? (int64_t)(w.r1 - w.r0) : p.red;
+                for (int kb = 0; kb < w.stages;) {
+                    const int acc = iter & 1;
+                    if (!wait_bar(ptx::smem_u32(&sh->tmem_empty[acc]), (uint32_t)((iter >> 1) & 1) ^ 1u, abort_flag,
+                                  p.dev_status)) {
                         ok = false;
                         break;
                     }
+                    ++iter;
                     ptx::tc_fence_after();
-                    const uint32_t sa = ptx::smem_u32(stage_base + stage * STAGE_BYTES), sb = sa + OPER_BYTES;
-                    const int64_t left = len - (int64_t)kb * BK;
-                    const int steps = left >= BK ? BK / 16 : (int)((left + 15) / 16);
-#pragma unroll
-                    for (int kk = 0; kk < BK / 16; ++kk) {
-                        if (kk < steps) {
-                            // K-major: 32 bytes along the row; MN-major: 16 rows of 128 bytes
-                            const uint64_t ad = C::A_MN ? ptx::make_sdesc(sa + 2048 * kk, BOX_BYTES, 1024, 2)
-                                                        : ptx::make_sdesc(sa + 32 * kk, 16, 1024, 2);
-                            const uint64_t bd = C::B_MN ? ptx::make_sdesc(sb + 2048 * kk, BOX_BYTES, 1024, 2)
-                                                        : ptx::make_sdesc(sb + 32 * kk, 16, 1024, 2);
-                            ptx::mma_bf16_pair(d, ad, bd, idesc, (kb | kk) != 0);
+                    const uint32_t d = tmem + (uint32_t)acc * TILE;
+                    const int kend = min(kb + w.chunk, w.stages);
+                    for (uint32_t first = 1; kb < kend; ++kb, first = 0) {
+                        if (!ready && !wait_bar(full0 + 8 * stage, phase, abort_flag, p.dev_status, false, MODE == WGRAD)) {
+                            ok = false;
+                            break;
                         }
+                        ptx::tc_fence_after();
+                        const uint64_t ad = a_desc + (uint64_t)(stage * (STAGE_BYTES >> 4));
+                        const uint64_t bd = b_desc + (uint64_t)(stage * (STAGE_BYTES >> 4));
+                        const uint32_t done = empty0 + 8 * stage;
+                        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                        // look at the next stage's barrier while this stage's MMAs are issued
+                        const bool peek = MODE == WGRAD ? ptx::mbar_test_wait_cluster(full0 + 8 * stage, phase)
+                                                        : ptx::mbar_test_wait(full0 + 8 * stage, phase);
+                        const int64_t left = len - (int64_t)kb * BK;
+                        // K-major: 32 bytes along the row per MMA; MN-major: 16 rows of 128 bytes
+                        constexpr uint64_t A_STEP = (A_MN ? 2048 : 32) >> 4, B_STEP = (B_MN ? 2048 : 32) >> 4;
+                        if (left >= BK) {
+#pragma unroll
+                            for (int kk = 0; kk < BK / 16; ++kk)
+                                if (one) ptx::mma_bf16_pair(d, ad + kk * A_STEP, bd + kk * B_STEP, idesc, kk == 0 ? 1u - first : 1u);
+                        } else {
+                            for (int kk = 0; 16 * kk < (int)left; ++kk)
+                                if (one) ptx::mma_bf16_pair(d, ad + kk * A_STEP, bd + kk * B_STEP, idesc, kk == 0 ? 1u - first : 1u);
+                        }
+                        if (one) ptx::tc_commit_pair_mc(done, 3);
+                        ready = __all_sync(0xffffffffu, peek ? 1 : 0) != 0;
+                        issued = true;
                     }
-                    ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->empty[stage]), 3);
-                    issued = true;
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    if (!ok) break;
+                    if (one) ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->tmem_full[acc]), 3);
+                    __syncwarp();
                 }
-                if (ok) ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->tmem_full[acc]), 3);
             }
             if (!ok && issued) {
                 // let every issued MMA finish before TMEM is released
-                ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->drain), 1);
+                if (one) ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->drain), 1);
                 wait_bar(ptx::smem_u32(&sh->drain), 0, abort_flag, p.dev_status, true);
             }
         }
         __syncwarp();
     } else if (warp == FIX_WARP) {
-        if (C::RAGGED_K) {
+        give_registers<MODE>();
+        if (MODE == WGRAD) {
             // --------------------- zero the surplus rows of ragged stages
             uint32_t stage = 0, parity = 0;             // one parity bit per stage's raw barrier
-            for (int64_t t = unit; t < total; t += n_units) {
+            for (int t = unit; t < total; t += n_units) {
                 const Tile w = tile_at<MODE>(p, sh, t);
                 if (w.stages == 0) continue;
                 const uint32_t s = (stage + (uint32_t)(w.stages - 1)) % STAGES;
                 stage = (s + 1) % STAGES;
                 const int rows = (w.r1 - w.r0) - (w.stages - 1) * BK;
                 if (rows == BK) continue;
-                bool ok = true;
-                if (lane == 0) ok = wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p.dev_status);
-                if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-                __syncwarp();
+                if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p.dev_status)) break;
                 parity ^= 1u << s;
                 uint8_t *base = stage_base + s * STAGE_BYTES;
-                constexpr int BOXES = MODE == KEPT ? 2 : 4;          // the converters zero their own operand
-                // 128-byte rows `rows`..63 of each box; the swizzle stays inside a row
+                // 128-byte rows `rows`..63 of both operands' boxes; the swizzle stays inside a row
                 for (int i = lane; i < (BK - rows) * 8; i += 32) {
 #pragma unroll
-                    for (int b = 0; b < BOXES; ++b)
+                    for (int b = 0; b < 4; ++b)
                         *reinterpret_cast<uint4 *>(base + b * BOX_BYTES + rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
                 }
                 ptx::fence_proxy_async_smem();
@@ -447,192 +530,105 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ 
                 if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0));
             }
         }
-    } else if (warp >= EPI_WARP0 && warp < EPI_WARP0 + EPI_WARPS) {
+    } else {
         // --------------------------------------------------- epilogue
+        // Warp w reads TMEM lanes 32 (w % 4).. of its CTA (M side) and one
+        // half of the columns (N side).
+        take_registers<MODE>();
         const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;
-        const int row_in_tile = (int)rank * 128 + q * 32 + lane;
+        const int m_in_tile = (int)rank * 128 + q * 32 + lane;
         int iter = 0;
-        for (int64_t t = unit; t < total; t += n_units) {
+        for (int t = unit; t < total; t += n_units) {
             const Tile w = tile_at<MODE>(p, sh, t);
-            const bool empty_sum = w.stages == 0;
-            if (empty_sum && p.accumulate) continue;
-            const int acc = iter & 1;
-            if (!empty_sum) {
+            const int64_t m = w.m0 + m_in_tile;
+            if (MODE == WGRAD) {
+                if (ADD && w.stages == 0) continue;
+                // row n of the gradient = TMEM column, its column k = lane
+                const int64_t n = w.n0 + half * 128;
+                const int64_t row = ((int64_t)w.split * p.E + w.e) * p.out_n + n;
+                const int rows = (int)(w.n_end - n);
+                float v[128];
+#pragma unroll
+                for (int i = 0; i < 128; ++i) v[i] = 0.0f;
                 bool ok = true;
-                if (lane == 0)
-                    ok = wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag,
-                                  p.dev_status);
-                if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-                __syncwarp();
+                for (int kb = w.chunk; kb < w.stages; kb += w.chunk, ++iter) {       // all chunks but the last
+                    const int acc = iter & 1;
+                    ok = wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)half * 128 + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t x[32];
+                        ptx::tmem_ld_32x32b_x32(src + c * 32, x);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[c * 32 + i] += __uint_as_float(x[i]);
+                    }
+                    // the accumulator is free once both CTAs' warps have read it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
+                }
+                if (!ok) break;
+                const int acc = iter & 1;
+                if (w.stages > 0) {
+                    if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status))
+                        break;
+                    ++iter;
+                    ptx::tc_fence_after();
+                }
+                // the last chunk's columns are stored as they are read: the stores
+                // drain while the next columns come
+                const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)half * 128 + ((uint32_t)(q * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    float y[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) y[i] = v[c * 32 + i];
+                    if (w.stages > 0) {
+                        uint32_t x[32];
+                        ptx::tmem_ld_32x32b_x32(src + c * 32, x);
+                        ptx::tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) y[i] += __uint_as_float(x[i]);
+                        if (c == 3) {
+                            ptx::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
+                        }
+                    }
+                    store_rows<ADD>(p, reinterpret_cast<OutT *>(p.out), row + c * 32, rows - c * 32, m, y);
+                    __syncwarp();                        // lanes without an output rejoin before the collective load
+                }
+            } else {
+                const int acc = iter & 1;
+                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status))
+                    break;
                 ++iter;
                 ptx::tc_fence_after();
-            }
-            const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)half * 128 + ((uint32_t)(q * 32) << 16);
-            const int64_t r = w.m0 + row_in_tile;
-            const bool live = r < w.m_end;
-            const int64_t orow = C::RAGGED_K ? ((int64_t)w.split * p.E + w.e) * p.out_m + r : r;
+                const int half_n = w.nt / 2;
+                const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)(half * half_n) + ((uint32_t)(q * 32) << 16);
+                // lane = output column m, TMEM columns = output rows
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t v[32];
-                __syncwarp();                            // lanes without a row rejoin before the collective load
-                if (!empty_sum) {
-                    ptx::tmem_ld_32x32b_x32(src + c * 32, v);
+                for (int c = 0; c < half_n; c += 32) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32x32b_x32(src + c, v);
                     ptx::tmem_ld_wait();
-                    if (c == 3) {
-                        // the accumulator is free once both CTAs' warps have read it
+                    if (c + 32 >= half_n) {
                         ptx::tc_fence_before();
                         __syncwarp();
                         if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
                     }
-                } else {
+                    const int64_t r = w.n0 + half * half_n + c;
+                    const int rows = (int)(w.n_end - r);
+                    float y[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0;
-                }
-                const int64_t col = w.n0 + half * 128 + c * 32;
-                if (!live || col >= p.out_n) continue;
-                const int64_t left = p.out_n - col;
-                if (p.out_f32) {
-                    float *dst = reinterpret_cast<float *>(p.out) + orow * p.ld_out + col;
-                    if (p.vec_bytes && left >= 32) {
-                        if (C::RAGGED_K && p.accumulate) {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float4 o = *reinterpret_cast<const float4 *>(dst + 4 * i);
-                                v[4 * i] = __float_as_uint(__uint_as_float(v[4 * i]) + o.x);
-                                v[4 * i + 1] = __float_as_uint(__uint_as_float(v[4 * i + 1]) + o.y);
-                                v[4 * i + 2] = __float_as_uint(__uint_as_float(v[4 * i + 2]) + o.z);
-                                v[4 * i + 3] = __float_as_uint(__uint_as_float(v[4 * i + 3]) + o.w);
-                            }
-                        }
-                        if (p.vec_bytes == 32) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) ptx::st_v8(dst + 8 * i, &v[8 * i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4 *>(dst + 4 * i) =
-                                    make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < left)
-                                dst[i] = C::RAGGED_K && p.accumulate ? dst[i] + __uint_as_float(v[i])
-                                                                     : __uint_as_float(v[i]);
-                    }
-                } else {
-                    __nv_bfloat16 *dst = reinterpret_cast<__nv_bfloat16 *>(p.out) + orow * p.ld_out + col;
-                    if (p.vec_bytes && left >= 32) {
-                        uint32_t o[16];
-                        if (C::RAGGED_K && p.accumulate) {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint4 old = *reinterpret_cast<const uint4 *>(dst + 8 * i);
-                                const uint32_t u[4] = {old.x, old.y, old.z, old.w};
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    v[8 * i + 2 * j] = __float_as_uint(__uint_as_float(v[8 * i + 2 * j]) + bf16lo(u[j]));
-                                    v[8 * i + 2 * j + 1] =
-                                        __float_as_uint(__uint_as_float(v[8 * i + 2 * j + 1]) + bf16hi(u[j]));
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = pack_bf16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        if (p.vec_bytes == 32) {
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) ptx::st_v8(dst + 16 * i, &o[8 * i]);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                *reinterpret_cast<uint4 *>(dst + 8 * i) =
-                                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (i < left) {
-                                float x = __uint_as_float(v[i]);
-                                if (C::RAGGED_K && p.accumulate) x += __bfloat162float(dst[i]);
-                                dst[i] = __float2bfloat16_rn(x);
-                            }
-                    }
+                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
+                    store_rows<false>(p, reinterpret_cast<OutT *>(p.out), r, rows, m, y);
+                    __syncwarp();                        // lanes without an output rejoin before the collective load
                 }
             }
-        }
-    } else if (MODE == KEPT && warp >= CONV_WARP0) {
-        // -------------------------------------------------- converters
-        // Warp w fills slot w: stages w, w + STAGES, ... of this CTA's sequence.  Lane
-        // layout of a 16-byte chunk (16 codes): 4 rows x 8 chunks a step, in
-        // an order whose shared stores touch every bank once.
-        const int cw = warp - CONV_WARP0;
-        const int chunk = (lane & 3) + 4 * ((lane >> 3) & 1);
-        const int rsub = ((lane >> 2) & 1) + 2 * (lane >> 4);
-        const uint32_t box = (uint32_t)(chunk >> 2) * BOX_BYTES;
-        const int q0 = 2 * (chunk & 3);
-        uint32_t seq = 0, ph = 0;
-        bool ok = true;
-        for (int64_t t = unit; ok && t < total; t += n_units) {
-            const Tile w = tile_at<MODE>(p, sh, t);
-            const int64_t col0 = w.n0 + rank * 128, col = col0 + chunk * 16;
-            const bool col_ok = col < p.out_n;
-            // seq: the slot of the tile's first stage
-            for (int kb = (cw + CONV_WARPS - (int)seq) % CONV_WARPS; kb < w.stages; kb += CONV_WARPS) {
-                const uint32_t s = (uint32_t)cw;
-                uint8_t *dst = stage_base + s * STAGE_BYTES + OPER_BYTES + box;
-#pragma unroll 1
-                for (int hf = 0; hf < 2; ++hf) {
-                    // 32 rows: lane l looks row l up, the codes then go 8 chunks a lane
-                    const int r = w.r0 + kb * BK + hf * 32 + lane;
-                    int64_t src = -1;
-                    uint32_t sw = 0;
-                    if (r < w.r1) {
-                        src = p.a_rows ? (int64_t)p.a_rows[r] : (int64_t)r;
-                        if (src >= p.T) src = -1;
-                    }
-                    if (src >= 0 && col0 < p.out_n)
-                        sw = __ldg(reinterpret_cast<const uint32_t *>(p.scales + src * p.ld_scales + (col0 >> 5)));
-                    uint4 code[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i * 4 + rsub;
-                        const int64_t sr = __shfl_sync(0xffffffffu, src, rr);
-                        code[i] = make_uint4(0, 0, 0, 0);
-                        if (sr >= 0 && col_ok) code[i] = load_codes(p.codes + sr * p.ld_codes + col, p.out_n - col);
-                    }
-                    if (hf == 0) {
-                        int good = 1;
-                        if (lane == 0)
-                            good = wait_bar(ptx::smem_u32(&sh->empty[s]), ph ^ 1u, abort_flag, p.dev_status);
-                        ok = __shfl_sync(0xffffffffu, good, 0) != 0;
-                        __syncwarp();
-                        if (!ok) break;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int rr = i * 4 + rsub, row = hf * 32 + rr;
-                        const uint32_t word = __shfl_sync(0xffffffffu, sw, rr);
-                        const uint32_t sc = kept_scale((word >> (8 * (chunk >> 1))) & 0xFFu);
-                        const uint32_t cw4[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
-                        uint32_t o[8];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            o[2 * j] = kept_pair(__byte_perm(cw4[j], 0u, 0x1404), sc);
-                            o[2 * j + 1] = kept_pair(__byte_perm(cw4[j], 0u, 0x3424), sc);
-                        }
-                        uint8_t *line = dst + row * 128;
-                        *reinterpret_cast<uint4 *>(line + ((q0 ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                        *reinterpret_cast<uint4 *>(line + (((q0 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                }
-                if (!ok) break;
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0));
-                ph ^= 1u;
-            }
-            seq = (seq + (uint32_t)w.stages) % STAGES;
         }
     }
 
@@ -664,13 +660,13 @@ __global__ void __launch_bounds__(256) k_wgrad_reduce(const float *__restrict__ 
 
 // ----------------------------------------------------------------- host side
 
-template <int MODE>
-static nvfp4_status launch(const CUtensorMap &tm_a, const CUtensorMap &tm_b, const Params &p, int64_t max_tiles,
+template <int MODE, typename OutT, bool ADD>
+static nvfp4_status launch(const CUtensorMap &tm_m, const CUtensorMap &tm_n, const Params &p, int64_t max_tiles,
                            cudaStream_t st)
 {
     static std::once_flag once[64];
     static cudaError_t attr_err[64];
-    auto kern = k_ragged_gemm<MODE>;
+    auto kern = k_ragged_gemm<MODE, OutT, ADD>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("k_ragged_gemm: device");
     std::call_once(once[dev], [&] {
@@ -682,7 +678,7 @@ static nvfp4_status launch(const CUtensorMap &tm_a, const CUtensorMap &tm_b, con
     cudaLaunchAttribute attr[1];
     const int64_t units = std::min<int64_t>(num_sms() / 2, max_tiles);
     cfg.gridDim = dim3((unsigned)(2 * units));
-    cfg.blockDim = dim3(Cfg<MODE>::THREADS);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = SMEM;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -691,16 +687,12 @@ static nvfp4_status launch(const CUtensorMap &tm_a, const CUtensorMap &tm_b, con
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kern, tm_a, tm_b, p);
+    cudaLaunchKernelEx(&cfg, kern, tm_m, tm_n, p);
     return check_launch("k_ragged_gemm");
 }
 
-// Widest vector store for rows of `row_bytes` from `base`.
-static int store_width(const void *base, int64_t row_bytes)
-{
-    const uintptr_t a = reinterpret_cast<uintptr_t>(base) | (uintptr_t)row_bytes;
-    return a % 32 == 0 ? 32 : a % 16 == 0 ? 16 : 0;
-}
+// Rows of bf16 pairs on 4 bytes?
+static int pair_stores(const void *base, int64_t ld) { return (reinterpret_cast<uintptr_t>(base) & 3u) == 0 && ld % 2 == 0; }
 
 // Row splits of a weight gradient: enough tiles for every CTA pair, but no
 // split shorter than 256 rows of an even segment.
@@ -737,37 +729,44 @@ extern "C" nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t 
     NVFP4_REQUIRE(ld_out >= outw, NVFP4_ERR_ALIGNMENT, "moe_ragged_gemm: ld_out must be >= the output width");
     NVFP4_REQUIRE(aligned16(a_dev) && aligned16(w_dev), NVFP4_ERR_ALIGNMENT,
                   "moe_ragged_gemm: a and w must be 16-byte aligned");
-    CUtensorMap tm_a, tm_b;
+    CUtensorMap tm_m, tm_n;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const bool ok = make_tmap_2d(&tm_a, a_dev, bf, (uint64_t)in, (uint64_t)M, (uint64_t)lda * 2, 64, 128, sw) &&
-                    make_tmap_3d(&tm_b, w_dev, bf, (uint64_t)K, (uint64_t)N, (uint64_t)E, (uint64_t)K * 2,
-                                 (uint64_t)N * K * 2, 64, transpose ? 64 : 128, sw);
+    const bool ok = make_tmap_2d(&tm_n, a_dev, bf, (uint64_t)in, (uint64_t)M, (uint64_t)lda * 2, BK, ROW_BOX, sw) &&
+                    make_tmap_3d(&tm_m, w_dev, bf, (uint64_t)K, (uint64_t)N, (uint64_t)E, (uint64_t)K * 2,
+                                 (uint64_t)N * K * 2, 64, transpose ? BK : 128, sw);
     NVFP4_REQUIRE(ok, NVFP4_ERR_CUDA, "moe_ragged_gemm: tensor map encoding failed");
     Params p{};
     p.M = M;
-    p.out_n = outw;
+    p.out_m = outw;
     p.red = in;
     p.E = E;
-    p.n_tiles = (int)((outw + TILE - 1) / TILE);
+    p.m_tiles = (int)((outw + TILE - 1) / TILE);
     p.splits = 1;
     p.offsets = offsets_dev;
     p.out = out_dev;
     p.ld_out = ld_out;
-    p.out_f32 = out_f32 ? 1 : 0;
-    p.vec_bytes = store_width(out_dev, ld_out * (out_f32 ? 4 : 2));
+    p.pairs = pair_stores(out_dev, ld_out);
     p.dev_status = dev_status;
     // row tiles: at most one partial tile per expert that has rows
-    const int64_t max_tiles = (M / TILE + std::min<int64_t>(E, M)) * p.n_tiles;
+    const int64_t max_tiles = (M / TILE + std::min<int64_t>(E, M)) * p.m_tiles;
+    NVFP4_REQUIRE(max_tiles < (1ll << 30), NVFP4_ERR_UNSUPPORTED_SHAPE, "moe_ragged_gemm: too many tiles");
     cudaStream_t st = (cudaStream_t)stream;
-    return transpose ? launch<DGRAD>(tm_a, tm_b, p, max_tiles, st) : launch<FWD>(tm_a, tm_b, p, max_tiles, st);
+    if (transpose)
+        return out_f32 ? launch<DGRAD, float, false>(tm_m, tm_n, p, max_tiles, st)
+                       : launch<DGRAD, __nv_bfloat16, false>(tm_m, tm_n, p, max_tiles, st);
+    return out_f32 ? launch<FWD, float, false>(tm_m, tm_n, p, max_tiles, st)
+                   : launch<FWD, __nv_bfloat16, false>(tm_m, tm_n, p, max_tiles, st);
 }
 
-extern "C" size_t moe_ragged_wgrad_workspace_size(int64_t M, int64_t N, int64_t K, int32_t E)
+// Workspace of a weight gradient: [BF16 copy of the kept rows][partial results].
+static size_t expanded_bytes(int64_t M, int64_t K) { return ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
+
+extern "C" size_t moe_ragged_wgrad_workspace_size(int64_t M, int64_t N, int64_t K, int32_t E, int32_t kept)
 {
     if (M <= 0 || N <= 0 || K <= 0 || E <= 0) return 0;
     const int s = nvfp4::ragged::wgrad_splits(M, N, K, E);
-    return s > 1 ? (size_t)s * (size_t)E * (size_t)N * (size_t)K * 4 : 0;
+    return (kept ? expanded_bytes(M, K) : 0) + (s > 1 ? (size_t)s * (size_t)E * (size_t)N * (size_t)K * 4 : 0);
 }
 
 extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev, int64_t lda,
@@ -806,44 +805,54 @@ extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t
     NVFP4_REQUIRE(aligned16(g_dev) && aligned16(a_dev) && aligned16(a_scales_dev), NVFP4_ERR_ALIGNMENT,
                   "moe_ragged_wgrad: pointers must be 16-byte aligned");
     const int splits = wgrad_splits(M, N, K, E);
-    const size_t need = moe_ragged_wgrad_workspace_size(M, N, K, E);
+    const size_t need = moe_ragged_wgrad_workspace_size(M, N, K, E, kept ? 1 : 0);
     NVFP4_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && aligned16(workspace)), NVFP4_ERR_WORKSPACE,
                   "moe_ragged_wgrad: workspace of %zu bytes required", need);
 
-    CUtensorMap tm_a, tm_b;
+    const int64_t max_tiles = (int64_t)E * ((K + TILE - 1) / TILE) * ((N + TILE - 1) / TILE) * splits;
+    NVFP4_REQUIRE(max_tiles < (1ll << 30), NVFP4_ERR_UNSUPPORTED_SHAPE, "moe_ragged_wgrad: too many tiles");
+    uint8_t *partials = reinterpret_cast<uint8_t *>(workspace);
+    if (kept) {
+        // the kept rows as BF16, in row order
+        const int64_t ld = (K + 7) / 8 * 8;
+        const nvfp4_status rc = act8_expand(reinterpret_cast<const uint8_t *>(a_dev), lda, a_scales_dev, ld_scales,
+                                            a_rows_dev, T, M, K, workspace, ld, st);
+        if (rc != NVFP4_OK) return rc;
+        a_dev = workspace;
+        lda = ld;
+        partials += expanded_bytes(M, K);
+    }
+    CUtensorMap tm_m, tm_n;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    bool ok = make_tmap_2d(&tm_a, g_dev, bf, (uint64_t)N, (uint64_t)M, (uint64_t)ldg * 2, 64, 64, sw);
-    if (!kept) ok = ok && make_tmap_2d(&tm_b, a_dev, bf, (uint64_t)K, (uint64_t)M, (uint64_t)lda * 2, 64, 64, sw);
-    else tm_b = tm_a;
+    const bool ok = make_tmap_2d(&tm_m, a_dev, bf, (uint64_t)K, (uint64_t)M, (uint64_t)lda * 2, 64, BK, sw) &&
+                    make_tmap_2d(&tm_n, g_dev, bf, (uint64_t)N, (uint64_t)M, (uint64_t)ldg * 2, 64, BK, sw);
     NVFP4_REQUIRE(ok, NVFP4_ERR_CUDA, "moe_ragged_wgrad: tensor map encoding failed");
     Params p{};
     p.M = M;
-    p.out_m = N;
-    p.out_n = K;
+    p.out_m = K;
+    p.out_n = N;
     p.E = E;
-    p.n_tiles = (int)((K + TILE - 1) / TILE);
-    p.m_tiles = (int)((N + TILE - 1) / TILE);
+    p.m_tiles = (int)((K + TILE - 1) / TILE);
+    p.n_tiles = (int)((N + TILE - 1) / TILE);
     p.splits = splits;
     p.offsets = offsets_dev;
-    p.out = splits > 1 ? workspace : out_dev;
+    p.out = splits > 1 ? partials : out_dev;
     p.ld_out = K;
-    p.out_f32 = splits > 1 || out_f32 ? 1 : 0;
-    p.accumulate = splits > 1 ? 0 : (accumulate ? 1 : 0);
-    p.vec_bytes = store_width(p.out, K * (p.out_f32 ? 4 : 2));
-    p.codes = reinterpret_cast<const uint8_t *>(a_dev);
-    p.ld_codes = lda;
-    p.scales = a_scales_dev;
-    p.ld_scales = ld_scales;
-    p.a_rows = a_rows_dev;
-    p.T = T;
+    p.pairs = pair_stores(p.out, K);
     p.dev_status = dev_status;
-    const int64_t max_tiles = (int64_t)E * p.m_tiles * p.n_tiles * splits;
-    const nvfp4_status rc = kept ? launch<KEPT>(tm_a, tm_b, p, max_tiles, st) : launch<WGRAD>(tm_a, tm_b, p, max_tiles, st);
-    if (rc != NVFP4_OK || splits == 1) return rc;
+    if (splits == 1) {
+        if (out_f32)
+            return accumulate ? launch<WGRAD, float, true>(tm_m, tm_n, p, max_tiles, st)
+                              : launch<WGRAD, float, false>(tm_m, tm_n, p, max_tiles, st);
+        return accumulate ? launch<WGRAD, __nv_bfloat16, true>(tm_m, tm_n, p, max_tiles, st)
+                          : launch<WGRAD, __nv_bfloat16, false>(tm_m, tm_n, p, max_tiles, st);
+    }
+    const nvfp4_status rc = launch<WGRAD, float, false>(tm_m, tm_n, p, max_tiles, st);
+    if (rc != NVFP4_OK) return rc;
     const int64_t n = (int64_t)E * N * K;
     const unsigned blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, (int64_t)num_sms() * 8));
-    k_wgrad_reduce<<<blocks, 256, 0, st>>>(reinterpret_cast<const float *>(workspace), splits, n, out_dev,
+    k_wgrad_reduce<<<blocks, 256, 0, st>>>(reinterpret_cast<const float *>(partials), splits, n, out_dev,
                                            out_f32 ? 1 : 0, accumulate ? 1 : 0);
     return check_launch("k_wgrad_reduce");
 }

@@ -22,6 +22,8 @@ library's kernels plus one memset of Y.
 """
 from __future__ import annotations
 
+import dataclasses
+
 import torch
 
 from . import api
@@ -153,6 +155,21 @@ class MoELayerW4A4:
                          epilogue=api.EPI_SCATTER_ADD_F32, row_token=r.row_token, row_gate=r.row_gate, out=self.y)
         return self.y
 
+    def decode(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+        """The layer for the few tokens of a decode step (any number of rows,
+        not the constructor's): the same NVFP4 weights, activations in BF16
+        (W4A16: nothing is quantized or compensated), two matrix-vector
+        launches after the routing.  x bf16 [t, H], logits f32 [t, E]; returns
+        f32 [t, H], a new tensor.  Bound by the weights of the experts in use;
+        from a few dozen tokens on, forward's grouped GEMM is the faster form."""
+        if logits.shape[0] == 0:
+            return torch.empty(0, self.H, dtype=torch.float32, device=x.device)
+        r = api.route(logits, self.k_r, seg_align=1)
+        h = api.nvfp4_gemv(x, self.c13, self.sf13, self.s13, 2 * self.I, self.H, expert_idx=r.topk_idx,
+                           epilogue=api.EPI_SWIGLU_BF16)
+        return api.nvfp4_gemv(h, self.c2, self.sf2, self.s2, self.H, self.I, expert_idx=r.topk_idx,
+                              epilogue=api.EPI_COMBINE_F32, gate=r.topk_gate)
+
     def _route_into(self, logits):
         lib = api._lib.load()
         r = self.routing
@@ -166,6 +183,15 @@ class MoELayerW4A4:
         return r
 
 
+@dataclasses.dataclass
+class LayerGrads:
+    """Gradients of MoELayerW4A16 (f32)."""
+    dx: torch.Tensor            # [T, H]
+    dlogits: torch.Tensor       # [T, E]
+    dw13: torch.Tensor          # [E, 2I, H], of the fake-quantized weights (straight through to the bf16 ones)
+    dw2: torch.Tensor           # [E, H, I]
+
+
 class MoELayerW4A16:
     """Trainer-side asymmetric QAT layer (gist.science/it 2.2 A): the expert
     weights are fake-quantized to NVFP4 (nvfp4_qdq_weights: bf16 ->
@@ -177,6 +203,10 @@ class MoELayerW4A16:
       3. BF16 grouped GEMM       X Wq13^T, epilogue SwiGLU -> h bf16
       4. BF16 grouped GEMM       h Wq2^T, epilogue router-weighted scatter-add
                                  into Y [T x H] fp32
+
+    forward_train / backward are the training step's pair: unpadded ragged
+    segments, X and the SwiGLU's inputs kept in 8 bits in between, no atomics
+    (the same inputs give the same bits).
     """
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, tokens: int, topk: int, seg_align: int = 256):
@@ -223,6 +253,59 @@ class MoELayerW4A16:
                               epilogue=api.EPI_SCATTER_ADD_F32, row_token=r.row_token, row_gate=r.row_gate,
                               out=self.y)
         return self.y
+
+    def _train_buffers(self, dev):
+        """Routed rows of the training pair, made at the first forward_train."""
+        m, H, I = self.T * self.k_r, self.H, self.I
+        bf = dict(dtype=torch.bfloat16, device=dev)
+        self.rows_h = torch.empty(m, H, **bf)           # routed X, later routed dY
+        self.rows_y = torch.empty(m, H, **bf)           # down rows, later dX rows
+        self.y13 = torch.empty(m, 2 * I, **bf)          # gate/up rows, later their gradient
+        self.h_t = torch.empty(m, I, **bf)              # h, later its gradient
+        self.gh = torch.empty(m, I, **bf)               # router-weighted h
+        self.dgate = torch.empty(m, dtype=torch.float32, device=dev)
+        self.x8 = api._act8_empty(self.T, H, dev)       # kept between forward_train and backward
+        self.y8 = api._act8_empty(m, 2 * I, dev)
+
+    def forward_train(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
+        """The layer with what backward needs kept in 8 bits: X (per token, not
+        per routed copy) and the gate/up rows.  Returns Y f32 [T, H], a new
+        tensor.  I must be a multiple of 32."""
+        if tuple(x.shape) != (self.T, self.H) or tuple(logits.shape) != (self.T, self.E):
+            raise ValueError(f"forward_train: need x [{self.T}, {self.H}] and logits [{self.T}, {self.E}], got "
+                             f"{tuple(x.shape)} and {tuple(logits.shape)}")
+        if not hasattr(self, "x8"):
+            self._train_buffers(x.device)
+        r = self.train_routing = api.route(logits, self.k_r, seg_align=1)
+        api.act8_quantize(x, out=self.x8)
+        api.routed_rows_bf16(x, r.row_token, r.m_pad_max, out=self.rows_h)
+        api.ragged_gemm(self.rows_h, self.wq13, r.offsets, out=self.y13)
+        api.swiglu_act8(self.y13, h=self.h_t, out=self.y8)
+        api.ragged_gemm(self.h_t, self.wq2, r.offsets, out=self.rows_y)
+        return api.combine_rows(self.rows_y, r.dst_row, gate=r.topk_gate)
+
+    def backward(self, dy: torch.Tensor, *, dw13: torch.Tensor | None = None, dw2: torch.Tensor | None = None,
+                 accumulate: bool = False) -> LayerGrads:
+        """Gradients of the last forward_train for dY (bf16 [T, H]), with its
+        weights (call it before set_weights).  dw13 / dw2: where the weight
+        gradients go (f32 or bf16); accumulate adds to them."""
+        r = getattr(self, "train_routing", None)
+        if r is None:
+            raise RuntimeError("backward: no forward_train to differentiate")
+        if tuple(dy.shape) != (self.T, self.H) or dy.dtype != torch.bfloat16:
+            raise ValueError(f"backward: dy must be bf16 [{self.T}, {self.H}]")
+        if accumulate and (dw13 is None or dw2 is None):
+            raise ValueError("backward: accumulate needs dw13 and dw2")
+        # routed dY; u = dY W2, the gradient of h before the router's weight
+        api.routed_rows_bf16(dy, r.row_token, r.m_pad_max, out=self.rows_h)
+        api.ragged_gemm(self.rows_h, self.wq2, r.offsets, transpose=True, out=self.h_t)
+        api.swiglu_act8_backward(self.y8, self.h_t, row_gate=r.row_gate, dy=self.y13, gh=self.gh, dgate=self.dgate)
+        dw2 = api.ragged_wgrad(self.rows_h, self.gh, r.offsets, out=dw2, accumulate=accumulate)
+        dw13 = api.ragged_wgrad(self.y13, self.x8, r.offsets, a_rows=r.row_token, out=dw13, accumulate=accumulate)
+        api.ragged_gemm(self.y13, self.wq13, r.offsets, transpose=True, out=self.rows_y)
+        dx = api.combine_rows(self.rows_y, r.dst_row)
+        dlogits = api.route_backward(r.topk_idx, r.topk_gate, r.dst_row, self.dgate, self.E)
+        return LayerGrads(dx, dlogits, dw13, dw2)
 
     _route_into = MoELayerW4A4._route_into
 
@@ -297,3 +380,8 @@ class DenseLayerW4A4:
                          r.offsets, rac_ld=self.rac_ld, rho=xq.r_sel, w_sel=self.w_sel,
                          epilogue=api.EPI_STORE_F32, row_token=r.row_token, row_gate=r.row_gate, out=self.out)
         return self.out[: self.T]
+
+    def decode(self, x: torch.Tensor) -> torch.Tensor:
+        """A few rows' product with the same NVFP4 weight, activations in BF16
+        (any number of rows); f32 [rows, N], a new tensor."""
+        return api.nvfp4_gemv(x, self.c_w, self.sf_w, self.s_w, self.N, self.K)

@@ -165,7 +165,7 @@ def test_weight_gradient_keeps_bad_values_apart(cuda):
 def test_weight_gradient_split_rows(cuda, E, M, N, K):
     """Few output tiles: rows split over the SMs, partial sums through the
     workspace; the same bits from run to run."""
-    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, E) > 0
+    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, E, 0) > 0
     cut = sorted([0] + [int(M * f) for f in (0.13, 0.52)][: E - 1] + [M - 3])
     off = torch.tensor(cut, dtype=I32, device=cuda)
     g, a = rnd(16, M, -(-N // 8) * 8, scale=0.1)[:, :N], rnd(17, M, K)

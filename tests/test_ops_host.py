@@ -48,19 +48,21 @@ def test_ragged_wgrad():
         (4, 248, ALIGN), (4, 260, ALIGN), (0, ODD, ALIGN), (3, ODD, ALIGN), (7, FAKE, INVALID)])
     kept = list(good)
     kept[5], kept[6], kept[8] = FAKE, 8, 5000
+    kept[16], kept[17] = FAKE, 1000
     calls("moe_ragged_wgrad", kept, [(6, 4, ALIGN), (6, 9, ALIGN), (4, 264, ALIGN), (8, 4999, INVALID),
-                                     (5, ODD, ALIGN)])
+                                     (5, ODD, ALIGN), (16, None, WORKSPACE)])
+    assert _lib.load().moe_ragged_wgrad_workspace_size(5000, 256, 256, 128, 1) == 5000 * 256 * 2
     # few output tiles: a workspace is required
     lib = _lib.load()
     few = list(good)
     few[11] = 1
-    need = lib.moe_ragged_wgrad_workspace_size(5000, 256, 256, 1)
+    need = lib.moe_ragged_wgrad_workspace_size(5000, 256, 256, 1, 0)
     assert need > 0
     assert lib.moe_ragged_wgrad(*few) == WORKSPACE
     few[16], few[17] = FAKE, need - 1
     assert lib.moe_ragged_wgrad(*few) == WORKSPACE
-    assert lib.moe_ragged_wgrad_workspace_size(5000, 4096, 4096, 1) == 0
-    assert lib.moe_ragged_wgrad_workspace_size(-1, 64, 64, 1) == 0
+    assert lib.moe_ragged_wgrad_workspace_size(5000, 4096, 4096, 1, 0) == 0
+    assert lib.moe_ragged_wgrad_workspace_size(-1, 64, 64, 1, 0) == 0
     # empty results and empty sums into an accumulator
     none = list(good)
     none[9] = 0
