@@ -623,13 +623,18 @@ NVFP4_API nvfp4_status moe_route_backward(const int32_t *topk_idx_dev, const flo
  * one dense weight (E = 1, k_r = 1), eight tokens sharing each weight read.
  * x_dev bf16 [rows x ldx]; codes, scales, s_t as nvfp4_qdq_weights writes
  * them for E tensors [N x K].  K % 64 == 0, any N (even for SwiGLU), ldx % 8
- * == 0, k_r <= 32; x, codes and scales 16-byte aligned.  Any T; meant for the
- * few tokens of a decode step (each token reads its experts' weights).
+ * == 0, k_r <= 32; x, codes and scales 16-byte aligned.  Tokens that name the
+ * same expert share its weights, eight at a time.  Any T; meant for the few
+ * tokens of a decode step.  workspace: moe_nvfp4_gemv_workspace_size bytes (0
+ * but for the combine of several tokens), 16-byte aligned.
  * -------------------------------------------------------------------------- */
+NVFP4_API size_t moe_nvfp4_gemv_workspace_size(int64_t T, int64_t N, int32_t E, int32_t k_r, int32_t epilogue);
+
 NVFP4_API nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx, const uint8_t *codes_dev,
                                       const uint8_t *scales_dev, const float *s_t_dev, int64_t N, int64_t K,
                                       int32_t E, const int32_t *expert_idx_dev, int32_t k_r, int32_t epilogue,
-                                      const float *gate_dev, void *out_dev, int64_t ld_out, void *stream);
+                                      const float *gate_dev, void *out_dev, int64_t ld_out, void *workspace,
+                                      size_t workspace_bytes, void *stream);
 
 /* --------------------------------------------------------------------------
  * nvfp4_debug_gemm_wait_expiry -- test hook for the bounded device waits of

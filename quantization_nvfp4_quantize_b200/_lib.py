@@ -86,8 +86,10 @@ SIGNATURES = {
                                    c_int64, c_void_p]),
     "moe_route_backward": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32, c_int32,
                                      c_void_p, c_void_p]),
+    "moe_nvfp4_gemv_workspace_size": (c_size_t, [c_int64, c_int64, c_int32, c_int32, c_int32]),
     "moe_nvfp4_gemv": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32,
-                                 c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_void_p]),
+                                 c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_void_p, c_size_t,
+                                 c_void_p]),
     "nvfp4_debug_gemm_wait_expiry": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                                c_int64, c_int64, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
                                                c_void_p, c_int64, c_void_p, c_int64, c_void_p]),

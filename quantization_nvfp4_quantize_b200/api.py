@@ -325,72 +325,82 @@ def w8a8_grouped_gemm(a_codes, a_s, m_pad_max, b_codes, b_s, N, K, E, offsets, *
     return out
 
 
-@dataclasses.dataclass
+@dataclasses.dataclass(slots=True)
 class Act8:
     """Activations kept in 8 bits (act8_quantize): value = e4m3(code) *
     2^(scale - 127), one scale per 32 columns of a row."""
     codes: torch.Tensor          # uint8 [M, K], row stride a multiple of 16
     scales: torch.Tensor         # uint8 [M, 4 * ceil(K / 128)]
 
-    @property
-    def device(self):
-        return self.codes.device
+    def get_device(self) -> int:
+        return self.codes.get_device()
+
+
+# The experts' training and decode operators.  Their short calls last a few
+# microseconds on the device, so the checks below are written to cost little.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_empty = torch.empty
 
 
 def _on_device(fn):
-    """Run with the first argument's device current (the library launches on
-    the current device)."""
+    """Refuse host tensors; run with the first argument's device current (the
+    library launches on the current device)."""
     @functools.wraps(fn)
     def call(x, *args, **kwargs):
-        d = x.device
-        if d.type == "cuda" and d.index != torch.cuda.current_device():
-            with torch.cuda.device(d):
+        i = x.get_device()
+        if i < 0:
+            raise ValueError("the NVFP4 kernels run on CUDA tensors only (got a tensor on cpu); there is no CPU path")
+        if i != _current_device():
+            with torch.cuda.device(i):
                 return fn(x, *args, **kwargs)
         return fn(x, *args, **kwargs)
     return call
 
 
-def _matrix(t, name, dtype, rows, cols, device):
-    """A [rows, cols] tensor of `dtype` on `device` with unit column stride
-    (rows None: any)."""
-    if t.dtype is not dtype or t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: need {dtype} [{'rows' if rows is None else rows}, {cols}], got {t.dtype} {tuple(t.shape)}")
-    if t.stride(1) != 1 and cols > 1:
+def _matrix(t, name, dtype, rows, cols, index):
+    """Row stride of a [rows, cols] tensor (rows None: any) of `dtype` on
+    device `index` with contiguous columns; a single row has none: its width
+    rounded up to 16."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype is not dtype or len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name}: need {dtype} [{'rows' if rows is None else rows}, {cols}], got {t.dtype} {tuple(shape)}")
+    if stride[1] != 1 and cols > 1:
         raise ValueError(f"{name}: columns must be contiguous")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    return t
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+    return stride[0] if shape[0] > 1 else -(-cols // 16) * 16
 
 
-def _vector(t, name, dtype, n, device):
+def _vector(t, name, dtype, n, index):
+    """Address of n contiguous elements."""
     if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: need contiguous {dtype} with {n} elements, got {t.dtype} {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    return t
+    if t.get_device() != index:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+    return t.data_ptr()
 
 
-def _ld(t):
-    """Row stride (a single row has none: its width rounded up to 16)."""
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 16) * 16
-
-
-def _act8(a: Act8, name, rows, cols, device):
-    _matrix(a.codes, name + ".codes", U8, rows, cols, device)
+def _act8(a: Act8, name, rows, cols, index):
+    """(row stride of the codes, of the scales)."""
+    ldc = _matrix(a.codes, name + ".codes", U8, rows, cols, index)
     s = a.scales
-    if s.dtype is not U8 or s.dim() != 2 or s.shape[0] != a.codes.shape[0] or s.shape[1] < -(-cols // 128) * 4 \
-            or s.stride(1) != 1:
+    shape, stride = s.shape, s.stride()
+    if s.dtype is not U8 or len(shape) != 2 or shape[0] != a.codes.shape[0] or shape[1] < -(-cols // 128) * 4 \
+            or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name}.scales: need uint8 [{a.codes.shape[0]}, {-(-cols // 128) * 4}], got {s.dtype} "
-                         f"{tuple(s.shape)}")
-    if s.device != device:
-        raise ValueError(f"{name}.scales: on {s.device}, expected {device}")
-    return a
+                         f"{tuple(shape)}")
+    if s.get_device() != index:
+        raise ValueError(f"{name}.scales: on {s.device}, expected cuda:{index}")
+    return ldc, stride[0] if shape[0] > 1 else -(-cols // 128) * 4
 
 
 def _act8_empty(M, K, device):
     ld = -(-K // 16) * 16
-    codes = torch.empty(M, ld, dtype=U8, device=device)
-    return Act8(codes if ld == K else codes[:, :K], torch.empty(M, -(-K // 128) * 4, dtype=U8, device=device))
+    codes = _empty(M, ld, dtype=U8, device=device)
+    return Act8(codes if ld == K else codes[:, :K], _empty(M, -(-K // 128) * 4, dtype=U8, device=device))
 
 
 @_on_device
@@ -402,25 +412,22 @@ def ragged_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, tran
     outside the segments are not written: pass `out` to keep what they hold
     (without it they are uninitialized)."""
     lib = _lib.load()
-    dev = a.device
-    stream = _stream(dev)
-    if w.dim() != 3 or w.dtype is not BF16 or not w.is_contiguous() or w.device != dev:
+    i = a.get_device()
+    if w.dim() != 3 or w.dtype is not BF16 or not w.is_contiguous() or w.get_device() != i:
         raise ValueError("ragged_gemm: w must be contiguous bf16 [E, N, K] on a's device")
     E, N, K = w.shape
-    _matrix(a, "ragged_gemm: a", BF16, None, N if transpose else K, dev)
-    M = a.shape[0]
     width = K if transpose else N
+    lda = _matrix(a, "ragged_gemm: a", BF16, None, N if transpose else K, i)
+    M = a.shape[0]
     if out is None:
         if out_dtype not in (BF16, F32):
             raise ValueError("ragged_gemm: out_dtype must be bfloat16 or float32")
-        out = torch.empty(M, width, dtype=out_dtype, device=dev)
-    elif out.dtype is F32:
-        _matrix(out, "ragged_gemm: out", F32, M, width, dev)
-    else:
-        _matrix(out, "ragged_gemm: out", BF16, M, width, dev)
-    _vector(offsets, "ragged_gemm: offsets", I32, E + 1, dev)
-    check(lib.moe_ragged_gemm(_p(a), _ld(a), M, _p(w), N, K, E, _p(offsets), 1 if transpose else 0, _p(out),
-                              _ld(out), 1 if out.dtype is F32 else 0, _p(dev_status), stream))
+        out = _empty(M, width, dtype=out_dtype, device=a.device)
+    f32 = out.dtype is F32
+    ldo = _matrix(out, "ragged_gemm: out", F32 if f32 else BF16, M, width, i)
+    check(lib.moe_ragged_gemm(a.data_ptr(), lda, M, w.data_ptr(), N, K, E,
+                              _vector(offsets, "ragged_gemm: offsets", I32, E + 1, i), transpose, out.data_ptr(), ldo,
+                              f32, _p(dev_status), _raw_stream(i)))
     return out
 
 
@@ -433,38 +440,35 @@ def ragged_wgrad(g: torch.Tensor, a, offsets: torch.Tensor, *, a_rows: torch.Ten
     a_rows[r] (int32 [M]; without it row r) belongs to row r.  accumulate adds
     to `out`."""
     lib = _lib.load()
-    dev = g.device
-    stream = _stream(dev)
+    i = g.get_device()
     if g.dim() != 2:
         raise ValueError("ragged_wgrad: g must be bf16 [M, N]")
     M, N = g.shape
-    _matrix(g, "ragged_wgrad: g", BF16, M, N, dev)
+    ldg = _matrix(g, "ragged_wgrad: g", BF16, M, N, i)
     E = offsets.numel() - 1
-    _vector(offsets, "ragged_wgrad: offsets", I32, E + 1, dev)
+    off = _vector(offsets, "ragged_wgrad: offsets", I32, E + 1, i)
     kept = isinstance(a, Act8)
     if kept:
         T, K = a.codes.shape
-        _act8(a, "ragged_wgrad: a", T if a_rows is not None else M, K, dev)
-        data, scales, lds = a.codes, a.scales, a.scales.stride(0)
+        lda, lds = _act8(a, "ragged_wgrad: a", T if a_rows is not None else M, K, i)
+        data, scales = a.codes.data_ptr(), a.scales.data_ptr()
     else:
-        K = a.shape[-1]
-        T = M
-        data, scales, lds = _matrix(a, "ragged_wgrad: a", BF16, M, K, dev), None, 0
-    if a_rows is not None:
-        _vector(a_rows, "ragged_wgrad: a_rows", I32, M, dev)
+        T, K = M, a.shape[-1]
+        lda, lds = _matrix(a, "ragged_wgrad: a", BF16, M, K, i), 0
+        data, scales = a.data_ptr(), None
+    rows = None if a_rows is None else _vector(a_rows, "ragged_wgrad: a_rows", I32, M, i)
     if out is None:
         if accumulate:
             raise ValueError("ragged_wgrad: accumulate needs out")
         if out_dtype not in (BF16, F32):
             raise ValueError("ragged_wgrad: out_dtype must be bfloat16 or float32")
-        out = torch.empty(E, N, K, dtype=out_dtype, device=dev)
-    elif out.dtype not in (BF16, F32) or tuple(out.shape) != (E, N, K) or not out.is_contiguous() or out.device != dev:
+        out = _empty(E, N, K, dtype=out_dtype, device=g.device)
+    elif out.dtype not in (BF16, F32) or out.shape != (E, N, K) or not out.is_contiguous() or out.get_device() != i:
         raise ValueError(f"ragged_wgrad: out must be contiguous bf16 or f32 [{E}, {N}, {K}] on g's device")
     need = lib.moe_ragged_wgrad_workspace_size(M, N, K, E, kept)
-    ws = torch.empty(need, dtype=U8, device=dev) if need else None
-    check(lib.moe_ragged_wgrad(_p(g), _ld(g), M, _p(data), _ld(data), _p(scales), lds, _p(a_rows), T, N, K, E,
-                               _p(offsets), _p(out), 1 if out.dtype is F32 else 0, 1 if accumulate else 0, _p(ws),
-                               need, _p(dev_status), stream))
+    ws = _empty(need, dtype=U8, device=g.device) if need else None
+    check(lib.moe_ragged_wgrad(g.data_ptr(), ldg, M, data, lda, scales, lds, rows, T, N, K, E, off, out.data_ptr(),
+                               out.dtype is F32, accumulate, _p(ws), need, _p(dev_status), _raw_stream(i)))
     return out
 
 
@@ -472,15 +476,16 @@ def ragged_wgrad(g: torch.Tensor, a, offsets: torch.Tensor, *, a_rows: torch.Ten
 def act8_quantize(x: torch.Tensor, *, out: Act8 | None = None) -> Act8:
     """act8_quantize (see the header): bf16 [M, K] kept in 8 bits."""
     lib = _lib.load()
-    dev = x.device
-    stream = _stream(dev)
+    i = x.get_device()
     if x.dim() != 2:
         raise ValueError("act8_quantize: x must be bf16 [M, K]")
     M, K = x.shape
-    _matrix(x, "act8_quantize: x", BF16, M, K, dev)
-    out = _act8_empty(M, K, dev) if out is None else _act8(out, "act8_quantize: out", M, K, dev)
-    check(lib.act8_quantize(_p(x), M, K, _ld(x), _p(out.codes), _ld(out.codes), _p(out.scales), out.scales.stride(0),
-                            stream))
+    ldx = _matrix(x, "act8_quantize: x", BF16, M, K, i)
+    if out is None:
+        out = _act8_empty(M, K, x.device)
+    ldc, lds = _act8(out, "act8_quantize: out", M, K, i)
+    check(lib.act8_quantize(x.data_ptr(), M, K, ldx, out.codes.data_ptr(), ldc, out.scales.data_ptr(), lds,
+                            _raw_stream(i)))
     return out
 
 
@@ -488,17 +493,14 @@ def act8_quantize(x: torch.Tensor, *, out: Act8 | None = None) -> Act8:
 def act8_dequantize(a: Act8, *, out: torch.Tensor | None = None) -> torch.Tensor:
     """act8_dequantize: the kept values as bf16 [M, K] (exact)."""
     lib = _lib.load()
-    dev = a.device
-    stream = _stream(dev)
+    i = a.get_device()
     M, K = a.codes.shape
-    _act8(a, "act8_dequantize: a", M, K, dev)
+    ldc, lds = _act8(a, "act8_dequantize: a", M, K, i)
     if out is None:
-        ld = -(-K // 8) * 8
-        out = torch.empty(M, ld, dtype=BF16, device=dev)[:, :K]
-    else:
-        _matrix(out, "act8_dequantize: out", BF16, M, K, dev)
-    check(lib.act8_dequantize(_p(a.codes), _ld(a.codes), _p(a.scales), a.scales.stride(0), M, K, _p(out), _ld(out),
-                              stream))
+        out = _empty(M, -(-K // 8) * 8, dtype=BF16, device=a.codes.device)[:, :K]
+    ldx = _matrix(out, "act8_dequantize: out", BF16, M, K, i)
+    check(lib.act8_dequantize(a.codes.data_ptr(), ldc, a.scales.data_ptr(), lds, M, K, out.data_ptr(), ldx,
+                              _raw_stream(i)))
     return out
 
 
@@ -507,16 +509,20 @@ def swiglu_act8(y: torch.Tensor, *, h: torch.Tensor | None = None, out: Act8 | N
     """moe_swiglu_act8 (see the header): (h = silu(gate) * up, y kept in 8
     bits) of y = [gate | up], bf16 [M, 2I]."""
     lib = _lib.load()
-    dev = y.device
-    stream = _stream(dev)
+    i = y.get_device()
     if y.dim() != 2 or y.shape[1] % 2:
         raise ValueError("swiglu_act8: y must be bf16 [M, 2I]")
-    M, I = y.shape[0], y.shape[1] // 2
-    _matrix(y, "swiglu_act8: y", BF16, M, 2 * I, dev)
-    h = torch.empty(M, I, dtype=BF16, device=dev) if h is None else _matrix(h, "swiglu_act8: h", BF16, M, I, dev)
-    out = _act8_empty(M, 2 * I, dev) if out is None else _act8(out, "swiglu_act8: out", M, 2 * I, dev)
-    check(lib.moe_swiglu_act8(_p(y), M, I, _ld(y), _p(h), _ld(h), _p(out.codes), _ld(out.codes), _p(out.scales),
-                              out.scales.stride(0), stream))
+    M, K = y.shape
+    I = K // 2
+    ldy = _matrix(y, "swiglu_act8: y", BF16, M, K, i)
+    if h is None:
+        h = _empty(M, I, dtype=BF16, device=y.device)
+    if out is None:
+        out = _act8_empty(M, K, y.device)
+    ldh = _matrix(h, "swiglu_act8: h", BF16, M, I, i)
+    ldc, lds = _act8(out, "swiglu_act8: out", M, K, i)
+    check(lib.moe_swiglu_act8(y.data_ptr(), M, I, ldy, h.data_ptr(), ldh, out.codes.data_ptr(), ldc,
+                              out.scales.data_ptr(), lds, _raw_stream(i)))
     return h, out
 
 
@@ -528,23 +534,25 @@ def swiglu_act8_backward(y: Act8, dh: torch.Tensor, *, row_gate: torch.Tensor | 
     [M, I], dgate f32 [M]) from the kept y and the gradient dh bf16 [M, I] of
     the unweighted h."""
     lib = _lib.load()
-    dev = y.device
-    stream = _stream(dev)
+    i = y.get_device()
     if dh.dim() != 2:
         raise ValueError("swiglu_act8_backward: dh must be bf16 [M, I]")
     M, I = dh.shape
-    _matrix(dh, "swiglu_act8_backward: dh", BF16, M, I, dev)
-    _act8(y, "swiglu_act8_backward: y", M, 2 * I, dev)
-    if row_gate is not None:
-        _vector(row_gate, "swiglu_act8_backward: row_gate", F32, M, dev)
-    dy = torch.empty(M, 2 * I, dtype=BF16, device=dev) if dy is None else \
-        _matrix(dy, "swiglu_act8_backward: dy", BF16, M, 2 * I, dev)
-    gh = torch.empty(M, I, dtype=BF16, device=dev) if gh is None else \
-        _matrix(gh, "swiglu_act8_backward: gh", BF16, M, I, dev)
-    dgate = torch.empty(M, dtype=F32, device=dev) if dgate is None else \
-        _vector(dgate, "swiglu_act8_backward: dgate", F32, M, dev)
-    check(lib.moe_swiglu_act8_backward(_p(y.codes), _ld(y.codes), _p(y.scales), y.scales.stride(0), _p(dh), _ld(dh),
-                                       _p(row_gate), M, I, _p(dy), _ld(dy), _p(gh), _ld(gh), _p(dgate), stream))
+    lddh = _matrix(dh, "swiglu_act8_backward: dh", BF16, M, I, i)
+    ldc, lds = _act8(y, "swiglu_act8_backward: y", M, 2 * I, i)
+    gate = None if row_gate is None else _vector(row_gate, "swiglu_act8_backward: row_gate", F32, M, i)
+    dev = dh.device
+    if dy is None:
+        dy = _empty(M, 2 * I, dtype=BF16, device=dev)
+    if gh is None:
+        gh = _empty(M, I, dtype=BF16, device=dev)
+    if dgate is None:
+        dgate = _empty(M, dtype=F32, device=dev)
+    lddy = _matrix(dy, "swiglu_act8_backward: dy", BF16, M, 2 * I, i)
+    ldgh = _matrix(gh, "swiglu_act8_backward: gh", BF16, M, I, i)
+    check(lib.moe_swiglu_act8_backward(y.codes.data_ptr(), ldc, y.scales.data_ptr(), lds, dh.data_ptr(), lddh, gate, M,
+                                       I, dy.data_ptr(), lddy, gh.data_ptr(), ldgh,
+                                       _vector(dgate, "swiglu_act8_backward: dgate", F32, M, i), _raw_stream(i)))
     return dy, gh, dgate
 
 
@@ -554,18 +562,18 @@ def combine_rows(rows: torch.Tensor, dst_row: torch.Tensor, *, gate: torch.Tenso
     """moe_combine_rows: out[t] = sum_j gate[t, j] rows[dst_row[t, j]] (f32,
     slot order); rows bf16 [M, H], dst_row int32 [T, k_r]."""
     lib = _lib.load()
-    dev = rows.device
-    stream = _stream(dev)
+    i = rows.get_device()
     if rows.dim() != 2 or dst_row.dim() != 2:
         raise ValueError("combine_rows: rows must be bf16 [M, H], dst_row int32 [T, k_r]")
     M, H = rows.shape
     T, kr = dst_row.shape
-    _matrix(rows, "combine_rows: rows", BF16, M, H, dev)
-    _vector(dst_row, "combine_rows: dst_row", I32, T * kr, dev)
-    if gate is not None:
-        _vector(gate, "combine_rows: gate", F32, T * kr, dev)
-    out = torch.empty(T, H, dtype=F32, device=dev) if out is None else _matrix(out, "combine_rows: out", F32, T, H, dev)
-    check(lib.moe_combine_rows(_p(rows), M, H, _ld(rows), _p(dst_row), _p(gate), T, kr, _p(out), _ld(out), stream))
+    ldr = _matrix(rows, "combine_rows: rows", BF16, M, H, i)
+    if out is None:
+        out = _empty(T, H, dtype=F32, device=rows.device)
+    ldo = _matrix(out, "combine_rows: out", F32, T, H, i)
+    check(lib.moe_combine_rows(rows.data_ptr(), M, H, ldr, _vector(dst_row, "combine_rows: dst_row", I32, T * kr, i),
+                               None if gate is None else _vector(gate, "combine_rows: gate", F32, T * kr, i), T, kr,
+                               out.data_ptr(), ldo, _raw_stream(i)))
     return out
 
 
@@ -575,22 +583,20 @@ def route_backward(topk_idx: torch.Tensor, topk_gate: torch.Tensor, dst_row: tor
     """moe_route_backward: the router logits' gradient f32 [T, E] from the
     routed rows' gate gradients dgate_row f32 [M]."""
     lib = _lib.load()
-    dev = topk_idx.device
-    stream = _stream(dev)
+    i = topk_idx.get_device()
     if topk_idx.dim() != 2 or dgate_row.dim() != 1:
         raise ValueError("route_backward: topk_idx must be int32 [T, k_r], dgate_row float32 [M]")
     T, kr = topk_idx.shape
     M = dgate_row.numel()
-    _vector(topk_idx, "route_backward: topk_idx", I32, T * kr, dev)
-    _vector(topk_gate, "route_backward: topk_gate", F32, T * kr, dev)
-    _vector(dst_row, "route_backward: dst_row", I32, T * kr, dev)
-    _vector(dgate_row, "route_backward: dgate_row", F32, M, dev)
     if out is None:
-        out = torch.empty(T, E, dtype=F32, device=dev)
-    elif out.dtype is not F32 or tuple(out.shape) != (T, E) or not out.is_contiguous() or out.device != dev:
+        out = _empty(T, E, dtype=F32, device=topk_idx.device)
+    elif out.dtype is not F32 or out.shape != (T, E) or not out.is_contiguous() or out.get_device() != i:
         raise ValueError(f"route_backward: out must be contiguous float32 [{T}, {E}]")
-    check(lib.moe_route_backward(_p(topk_idx), _p(topk_gate), _p(dst_row), _p(dgate_row), M, T, E, kr, _p(out),
-                                 stream))
+    check(lib.moe_route_backward(_vector(topk_idx, "route_backward: topk_idx", I32, T * kr, i),
+                                 _vector(topk_gate, "route_backward: topk_gate", F32, T * kr, i),
+                                 _vector(dst_row, "route_backward: dst_row", I32, T * kr, i),
+                                 _vector(dgate_row, "route_backward: dgate_row", F32, M, i), M, T, E, kr,
+                                 out.data_ptr(), _raw_stream(i)))
     return out
 
 
@@ -604,38 +610,40 @@ def nvfp4_gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s_t: 
     dense weight.  x has one row per token (EPI_COMBINE_F32: per token and
     slot, with the router weights `gate` f32 [T, k_r])."""
     lib = _lib.load()
-    dev = x.device
-    stream = _stream(dev)
-    _matrix(x, "nvfp4_gemv: x", BF16, None, K, dev)
+    i = x.get_device()
+    ldx = _matrix(x, "nvfp4_gemv: x", BF16, None, K, i)
+    rows = x.shape[0]
     E = s_t.numel()
-    if codes.dtype is not U8 or not codes.is_contiguous() or codes.numel() * 2 != E * N * K or codes.device != dev:
+    if codes.dtype is not U8 or not codes.is_contiguous() or codes.numel() * 2 != E * N * K or codes.get_device() != i:
         raise ValueError(f"nvfp4_gemv: codes must be contiguous uint8 [{E}, {N}, {K // 2}] on x's device")
-    _vector(s_t, "nvfp4_gemv: s_t", F32, E, dev)
     if scales.dtype is not U8 or not scales.is_contiguous() or scales.numel() < E * scale_bytes(N, K) \
-            or scales.device != dev:
+            or scales.get_device() != i:
         raise ValueError(f"nvfp4_gemv: scales must be contiguous uint8 with {E * scale_bytes(N, K)} bytes on x's device")
+    combine = epilogue == EPI_COMBINE_F32
     if expert_idx is None:
-        T, kr = x.shape[0], 1
+        T, kr, idx = rows, 1, None
     else:
         if expert_idx.dim() != 2:
             raise ValueError("nvfp4_gemv: expert_idx must be int32 [T, k_r]")
         T, kr = expert_idx.shape
-        _vector(expert_idx, "nvfp4_gemv: expert_idx", I32, T * kr, dev)
-        if x.shape[0] != (T * kr if epilogue == EPI_COMBINE_F32 else T):
-            raise ValueError(f"nvfp4_gemv: x has {x.shape[0]} rows for {T} tokens with {kr} experts each")
+        idx = _vector(expert_idx, "nvfp4_gemv: expert_idx", I32, T * kr, i)
+        if rows != (T * kr if combine else T):
+            raise ValueError(f"nvfp4_gemv: x has {rows} rows for {T} tokens with {kr} experts each")
     if gate is not None:
-        if epilogue != EPI_COMBINE_F32:
+        if not combine:
             raise ValueError("nvfp4_gemv: gate goes with EPI_COMBINE_F32")
-        _vector(gate, "nvfp4_gemv: gate", F32, T * kr, dev)
-    rows = T if epilogue == EPI_COMBINE_F32 else T * kr
+        gate = _vector(gate, "nvfp4_gemv: gate", F32, T * kr, i)
     swiglu = epilogue == EPI_SWIGLU_BF16
-    width = N // 2 if swiglu else N
+    dtype, width = (BF16, N // 2) if swiglu else (F32, N)
+    orows = T if combine else T * kr
     if out is None:
-        out = torch.empty(rows, width, dtype=BF16 if swiglu else F32, device=dev)
-    else:
-        _matrix(out, "nvfp4_gemv: out", BF16 if swiglu else F32, rows, width, dev)
-    check(lib.moe_nvfp4_gemv(_p(x), T, _ld(x), _p(codes), _p(scales), _p(s_t), N, K, E, _p(expert_idx), kr, epilogue,
-                             _p(gate), _p(out), _ld(out), stream))
+        out = _empty(orows, width, dtype=dtype, device=x.device)
+    ldo = _matrix(out, "nvfp4_gemv: out", dtype, orows, width, i)
+    need = lib.moe_nvfp4_gemv_workspace_size(T, N, E, kr, epilogue) if combine else 0
+    ws = _empty(need, dtype=U8, device=x.device) if need else None
+    check(lib.moe_nvfp4_gemv(x.data_ptr(), T, ldx, codes.data_ptr(), scales.data_ptr(),
+                             _vector(s_t, "nvfp4_gemv: s_t", F32, E, i), N, K, E, idx, kr, epilogue, gate,
+                             out.data_ptr(), ldo, _p(ws), need, _raw_stream(i)))
     return out
 
 

@@ -27,6 +27,7 @@
 #include "common.cuh"
 
 #include <algorithm>
+#include <mutex>
 
 namespace nvfp4 {
 namespace gemv {
@@ -36,7 +37,10 @@ constexpr int THREADS = WARPS * 32;
 constexpr int ROWS = 16;                 // weight rows per warp tile
 constexpr int COLS = 8;                  // tokens per MMA
 
-enum Form { STORE = 0, SWIGLU = 1, COMBINE = 2 };
+constexpr int DEPTH = 4;                 // ring slots per warp: one chunk computed, DEPTH - 1 in flight
+constexpr int MAX_PAIRS = 1024;          // (token, slot) pairs per launch
+
+enum Form { STORE = 0, SWIGLU = 1 };
 
 struct Params {
     const __nv_bfloat16 *x;
@@ -46,18 +50,13 @@ struct Params {
     const float *s_t;
     int64_t N, K;
     int E;
-    const int32_t *idx;                  // [T x k_r] or null (one dense weight)
-    int64_t T;
+    const int32_t *idx;                  // experts of the pairs, or null (one dense weight)
+    int pairs;                           // (token, slot) pairs (dense: tokens)
     int k_r;
+    int x_div;                           // row of x = pair / x_div
     const float *gate;
     void *out;
     int64_t ld_out;
-};
-
-struct Step {
-    uint4 c[2];                          // codes of rows g, g + 8
-    uint32_t s[2];                       // their two scale bytes
-    uint4 x[4];
 };
 
 __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b)
@@ -100,192 +99,341 @@ __device__ __forceinline__ int64_t tile_row(int tile, int rr)
     return (int64_t)(tile >> 3) * 128 + 32 * (g & 3) + 4 * (tile & 7) + (g >> 2) + 2 * (rr >> 3);
 }
 
-// One expert's weight as a lane sees it.
-struct Lane {
-    const uint8_t *c[2];                 // codes of its two rows, or null
-    const uint8_t *s[2];                 // their scale words in column group 0
-    const __nv_bfloat16 *x;              // its token's row, or null
+// A lane's pointers at column 32 t into one 16-row set: codes and scale words
+// of row g; row g + 8 (two weight rows further) lies c2 / s2 bytes on.  A row
+// past the end reads an existing one; its sums are not stored.
+struct Set {
+    const uint8_t *c;
+    const uint8_t *s;
+    int32_t c2, s2;
 };
 
-__device__ __forceinline__ void load_step(Step &st, const Lane &l, int64_t k0, int64_t K)
+__device__ __forceinline__ Set set_of(const Params &p, int e, int tile, int64_t row_base, int64_t rows)
 {
-    const bool in = k0 < K;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        st.c[h] = make_uint4(0, 0, 0, 0);
-        st.s[h] = 0;
-        if (in && l.c[h]) {
-            st.c[h] = __ldg(reinterpret_cast<const uint4 *>(l.c[h] + (k0 >> 1)));
-            // scale column k0 / 16: 64-column atoms of 512 bytes, 4 bytes per row
-            st.s[h] = __ldg(reinterpret_cast<const uint16_t *>(l.s[h] + (k0 >> 6) * 512 + ((k0 >> 4) & 3)));
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        st.x[i] = make_uint4(0, 0, 0, 0);
-        if (in && l.x) st.x[i] = __ldg(reinterpret_cast<const uint4 *>(l.x + k0) + i);
-    }
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const int64_t r = tile_row(tile, g);
+    const int64_t n = row_base + min(r, rows - 1);
+    Set l;
+    l.c = p.codes + ((int64_t)e * p.N + n) * (p.K / 2) + 16 * t;
+    l.s = p.scales + (int64_t)e * (((p.N + 127) / 128) * 128 * (p.K / 16)) + sf_offset(n, 0, p.K) + (t >> 1) * 512;
+    const bool second = r + 2 < rows;
+    l.c2 = second ? (int32_t)p.K : 0;
+    // rows n and n + 2 share a 32-row quarter unless the set straddles one (SwiGLU's up rows)
+    l.s2 = second ? (int32_t)(sf_offset(n + 2, 0, p.K) - sf_offset(n, 0, p.K)) : 0;
+    return l;
 }
 
-__device__ __forceinline__ void compute_step(const Step &st, float (&acc)[2][4])
+// 128 columns of one set: codes c, scale byte pairs s of its two rows, the
+// lane's 32 x as pairs (i, i + 4) in xp.
+__device__ __forceinline__ void compute_chunk(const uint4 (&c)[2], const uint32_t (&s)[2], const uint32_t (&xp)[16],
+                                              float (&acc)[4])
 {
-    const uint32_t ca[4] = {st.c[0].x, st.c[0].y, st.c[0].z, st.c[0].w};
-    const uint32_t cb[4] = {st.c[1].x, st.c[1].y, st.c[1].z, st.c[1].w};
+    const uint32_t ca[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
+    const uint32_t cb[4] = {c[1].x, c[1].y, c[1].z, c[1].w};
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-        const uint32_t sa = scale_operand((st.s[0] >> (8 * blk)) & 0xFFu);
-        const uint32_t sb = scale_operand((st.s[1] >> (8 * blk)) & 0xFFu);
+        const uint32_t sa = scale_operand((s[0] >> (8 * blk)) & 0xFFu);
+        const uint32_t sb = scale_operand((s[1] >> (8 * blk)) & 0xFFu);
 #pragma unroll
         for (int q = 2 * blk; q < 2 * blk + 2; ++q) {
             uint32_t pa[4], pb[4];
             decode8(ca[q], pa);
             decode8(cb[q], pb);
-            // x pairs (i, i + 4)
-            const uint4 v = st.x[q];
-            const uint32_t x0 = __byte_perm(v.x, v.z, 0x5410), x1 = __byte_perm(v.x, v.z, 0x7632);
-            const uint32_t x2 = __byte_perm(v.y, v.w, 0x5410), x3 = __byte_perm(v.y, v.w, 0x7632);
-            mma16816(acc[0], bmul2(pa[0], sa), bmul2(pb[0], sb), bmul2(pa[1], sa), bmul2(pb[1], sb), x0, x1);
-            mma16816(acc[1], bmul2(pa[2], sa), bmul2(pb[2], sb), bmul2(pa[3], sa), bmul2(pb[3], sb), x2, x3);
+            mma16816(acc, bmul2(pa[0], sa), bmul2(pb[0], sb), bmul2(pa[1], sa), bmul2(pb[1], sb), xp[4 * q], xp[4 * q + 1]);
+            mma16816(acc, bmul2(pa[2], sa), bmul2(pb[2], sb), bmul2(pa[3], sa), bmul2(pb[3], sb), xp[4 * q + 2],
+                     xp[4 * q + 3]);
         }
     }
 }
 
-// Columns [128 ch0, ...) in steps of 128 * stride, the next step's loads in
-// flight while one is computed.
-__device__ __forceinline__ void dot_range(const Lane &l, int ch0, int stride, int chunks, int64_t K, float (&acc)[2][4])
+// One chunk's operands of a lane, in flight through shared memory: every lane
+// reads back only what it copied, so a group wait is all the synchronization.
+template <int SETS>
+struct Slot {
+    uint4 c[2 * SETS][32];               // codes of the lane's rows
+    uint32_t s[32][2 * SETS];            // their scale words (64 columns)
+};
+
+__device__ __forceinline__ void copy16(void *dst, const void *src)
 {
-    const int t = threadIdx.x & 3;
-    if (ch0 >= chunks) return;
-    Step cur, nxt;
-    load_step(cur, l, (int64_t)ch0 * 128 + 32 * t, K);
-    for (int ch = ch0; ch < chunks; ch += stride) {
-        if (ch + stride < chunks) load_step(nxt, l, (int64_t)(ch + stride) * 128 + 32 * t, K);
-        compute_step(cur, acc);
-        cur = nxt;
-    }
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
-__device__ __forceinline__ Lane lane_of(const Params &p, int e, int tile, int64_t row_base, int64_t row_end,
-                                        const __nv_bfloat16 *x)
+__device__ __forceinline__ void copy4(void *dst, const void *src)
 {
-    const int g = (threadIdx.x & 31) >> 2;
-    const int64_t sf_expert = ((p.N + 127) / 128) * 128 * (p.K / 16);
-    Lane l;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+// Chunks of 128 columns ch0, ch0 + stride, ... below `chunks`, of SETS row sets
+// against the same x; DEPTH - 1 chunks are in flight while one is computed.
+// x: the lane's token row at column 32 t, or null (zeros).
+template <int SETS>
+__device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS], const __nv_bfloat16 *x, int ch0,
+                                          int stride, int chunks, int64_t K, float (&acc)[SETS][4])
+{
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    const int n = ch0 < chunks ? (chunks - ch0 + stride - 1) / stride : 0;
+    auto inside = [&](int i) { return (int64_t)(ch0 + i * stride) * 128 + 32 * t < K; };
+    auto issue = [&](int i) {
+        if (i < n) {
+            // K is a multiple of 64: half of the last chunk may be missing.  A
+            // missing part reads columns 0..63 again, against zeros of x.
+            const bool in = inside(i);
+            const int64_t at = in ? ch0 + i * stride : 0;
+            const int64_t back = in ? 0 : t >> 1;
+            Slot<SETS> &slot = ring[i % DEPTH];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int64_t r = tile_row(tile, g + 8 * h);
-        const int64_t n = row_base + r;
-        const bool ok = e >= 0 && n < row_end;
-        l.c[h] = ok ? p.codes + ((int64_t)e * p.N + n) * (p.K / 2) : nullptr;
-        l.s[h] = ok ? p.scales + (int64_t)e * sf_expert + sf_offset(n, 0, p.K) : nullptr;
+            for (int k = 0; k < SETS; ++k) {
+                const uint8_t *pc = l[k].c + at * 64 - back * 32;
+                const uint8_t *ps = l[k].s + at * 1024 - back * 512;
+                copy16(&slot.c[2 * k][lane], pc);
+                copy16(&slot.c[2 * k + 1][lane], pc + l[k].c2);
+                copy4(&slot.s[lane][2 * k], ps);
+                copy4(&slot.s[lane][2 * k + 1], ps + l[k].s2);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    uint4 v[4];                          // zeros where the lane has no token
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
+    auto load_x = [&](int i) {
+        if (x != nullptr && i < n) {
+            if (inside(i)) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(x + (int64_t)(ch0 + i * stride) * 128);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = __ldg(src + k);
+            } else {                     // the missing half of the last chunk
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
+            }
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < DEPTH - 1; ++i) issue(i);
+    load_x(0);
+    for (int i = 0; i < n; ++i) {
+        issue(i + DEPTH - 1);
+        uint32_t xp[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            xp[4 * q] = __byte_perm(v[q].x, v[q].z, 0x5410);
+            xp[4 * q + 1] = __byte_perm(v[q].x, v[q].z, 0x7632);
+            xp[4 * q + 2] = __byte_perm(v[q].y, v[q].w, 0x5410);
+            xp[4 * q + 3] = __byte_perm(v[q].y, v[q].w, 0x7632);
+        }
+        load_x(i + 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        const Slot<SETS> &slot = ring[i % DEPTH];
+#pragma unroll
+        for (int k = 0; k < SETS; ++k) {
+            const uint4 c[2] = {slot.c[2 * k][lane], slot.c[2 * k + 1][lane]};
+            const uint32_t s[2] = {slot.s[lane][2 * k] >> (16 * (t & 1)), slot.s[lane][2 * k + 1] >> (16 * (t & 1))};
+            compute_chunk(c, s, xp, acc[k]);
+        }
     }
-    l.x = x;
-    return l;
+    asm volatile("cp.async.wait_group 0;" ::: "memory");          // nothing in flight when the ring is reused
 }
 
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + expf(-z)); }
 
-// blockIdx.x: (token, slot) pair / group of 8 tokens (dense) / token
-// (COMBINE), fastest, so that blocks that share an expert's rows run together
-// and meet in L2; blockIdx.y: tile of 16 rows.
+// STORE and SWIGLU.  A warp takes two 16-row sets (STORE: 32 output rows;
+// SWIGLU: 16 gate rows and their up rows) and one of `splits` interleaved
+// parts of the columns; a block's 8 warps are 8 / splits such row pairs.
+// blockIdx.x: (token, slot) pair (dense: group of 8 tokens), fastest, so that
+// blocks that share an expert's rows run together and meet in L2.  The block
+// of the first pair that names an expert serves every pair that does, 8 per
+// pass of its weights; the others leave at once.
 template <int FORM>
-__global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p)
+__global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p, int splits)
 {
-    __shared__ float part[WARPS][ROWS][COLS];
+    extern __shared__ __align__(16) uint8_t dyn[];
+    Slot<2> *ring = reinterpret_cast<Slot<2> *>(dyn) + (threadIdx.x >> 5) * DEPTH;
+    __shared__ float part[WARPS][2][ROWS][COLS];
+    __shared__ int list[MAX_PAIRS];
+    __shared__ int count;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int tile = blockIdx.y;
     const int chunks = (int)((p.K + 127) / 128);
-    const int64_t b = blockIdx.x;
-    const bool dense = p.idx == nullptr;
+    const int b = (int)blockIdx.x;
+    const int per_block = WARPS / splits;                        // row pairs
+    const int rp = (int)blockIdx.y * per_block + warp / splits;  // this warp's
+    const int split = warp % splits;
     const int64_t n_rows = FORM == SWIGLU ? p.N / 2 : p.N;       // output rows
-    float tot[4] = {0, 0, 0, 0};
-
-    if (FORM == COMBINE) {
-        // the token's (expert, chunk) pairs, dealt to the warps in order
-        const int units = p.k_r * chunks;
-        const int per = (units + WARPS - 1) / WARPS;
-        int u = warp * per;
-        const int u_end = min(u + per, units);
-        while (u < u_end) {
-            const int j = u / chunks, ch = u - j * chunks;
-            const int ch_end = min(chunks, ch + (u_end - u));
-            const int64_t pair = b * p.k_r + j;
-            const int e = dense ? 0 : p.idx[pair];
-            if (e >= 0 && e < p.E) {
-                const Lane l = lane_of(p, e, tile, 0, p.N, g == 0 ? p.x + pair * p.ldx : nullptr);
-                float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-                dot_range(l, ch, 1, ch_end, p.K, acc);
-                const float coef = p.gate ? p.gate[pair] * p.s_t[e] : p.s_t[e];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tot[i] += coef * (acc[0][i] + acc[1][i]);
-            }
-            u += ch_end - ch;
-        }
+    const bool dense = p.idx == nullptr;
+    int e = 0, members = 1, first = b;
+    bool listed = false;
+    if (dense) {
+        first = b * COLS;
+        members = min(COLS, p.pairs - first);
     } else {
-        int64_t tok;
-        int e = 0;
-        const __nv_bfloat16 *x = nullptr;
-        if (dense) {
-            tok = b * COLS + g;
-            if (tok < p.T) x = p.x + tok * p.ldx;
-        } else {
-            tok = b / p.k_r;
-            e = p.idx[b];
-            if (e < 0 || e >= p.E) e = -1;
-            if (g == 0) x = p.x + tok * p.ldx;
-        }
-        const int parts = FORM == SWIGLU ? WARPS / 2 : WARPS;      // warps that share one set of rows
-        const int64_t base = FORM == SWIGLU && warp >= parts ? p.N / 2 : 0;
-        if (e >= 0) {
-            const Lane l = lane_of(p, e, tile, base, base + n_rows, x);
-            float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-            dot_range(l, warp % parts, parts, chunks, p.K, acc);
-            const float coef = p.s_t[e];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tot[i] = coef * (acc[0][i] + acc[1][i]);
+        e = p.idx[b];
+        if (e < 0 || e >= p.E) {
+            e = -1;                                              // no such expert: zeros, for this pair alone
+        } else if (p.pairs > 1) {
+            if (warp == 0) {
+                int n = 0;
+                bool later = false;
+                for (int i0 = 0; i0 < p.pairs; i0 += 32) {
+                    const int i = i0 + lane;
+                    const bool same = i < p.pairs && p.idx[i] == e;
+                    const unsigned m = __ballot_sync(0xffffffffu, same);
+                    if (same) list[n + __popc(m & ((1u << lane) - 1u))] = i;
+                    n += __popc(m);
+                    later = later || __any_sync(0xffffffffu, same && i < b);
+                }
+                if (lane == 0) count = later ? 0 : n;
+            }
+            __syncthreads();
+            members = count;
+            listed = true;
+            if (members == 0) return;
         }
     }
-    part[warp][g][2 * t] = tot[0];
-    part[warp][g][2 * t + 1] = tot[1];
-    part[warp][g + 8][2 * t] = tot[2];
-    part[warp][g + 8][2 * t + 1] = tot[3];
-    __syncthreads();
-    // 16 rows x 8 columns; the operands carry 2^-9
-    if (threadIdx.x < ROWS * COLS) {
-        const int rr = threadIdx.x & 15, col = threadIdx.x >> 4;
-        const int64_t n = tile_row(tile, rr);
-        const int64_t orow = FORM != COMBINE && dense ? b * COLS + col : b;
-        const bool live = n < n_rows && (FORM != COMBINE && dense ? orow < p.T : col == 0);
-        if (live) {
-            if (FORM == SWIGLU) {
-                float a = 0.0f, u = 0.0f;
+    // STORE: the row pair's two sets are neighbouring tiles; SWIGLU: gate and up
+    const int tile0 = FORM == SWIGLU ? rp : 2 * rp, tile1 = FORM == SWIGLU ? rp : 2 * rp + 1;
+    for (int m0 = 0; m0 < members; m0 += COLS) {
+        float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        float coef = 0.0f;
+        if (e >= 0) {
+            const bool mine = m0 + g < members;
+            const int pair = mine ? (listed ? list[m0 + g] : first + m0 + g) : 0;
+            const Set l[2] = {set_of(p, e, tile0, 0, n_rows),
+                              set_of(p, e, tile1, FORM == SWIGLU ? n_rows : 0, n_rows)};
+            dot_range<2>(ring, l, mine ? p.x + (int64_t)(pair / p.x_div) * p.ldx + 32 * t : nullptr, split, splits, chunks, p.K, acc);
+            coef = 512.0f * p.s_t[e];                            // the operands carry 2^-9
+        }
+        if (m0 > 0) __syncthreads();                             // the last pass's sums have been read
 #pragma unroll
-                for (int w = 0; w < WARPS / 2; ++w) {
-                    a += part[w][rr][col];
-                    u += part[w + WARPS / 2][rr][col];
+        for (int i = 0; i < 2; ++i) {
+            *reinterpret_cast<float2 *>(&part[warp][i][g][2 * t]) = make_float2(coef * acc[i][0], coef * acc[i][1]);
+            *reinterpret_cast<float2 *>(&part[warp][i][g + 8][2 * t]) = make_float2(coef * acc[i][2], coef * acc[i][3]);
+        }
+        __syncthreads();
+        // one thread per (row, column of the 8) of a set, row pairs in turn
+        const int rr = threadIdx.x & 15, col = (threadIdx.x >> 4) & 7, set = threadIdx.x >> 7;
+        if (m0 + col < members && (FORM == STORE || set == 0)) {
+            const int64_t orow = listed ? list[m0 + col] : first + m0 + col;
+            for (int j = 0; j < per_block; ++j) {
+                const int orp = (int)blockIdx.y * per_block + j;
+                const int64_t n = tile_row(FORM == SWIGLU ? orp : 2 * orp + set, rr);
+                if (n >= n_rows) continue;
+                float y = 0.0f, u = 0.0f;
+                for (int w = j * splits; w < (j + 1) * splits; ++w) {
+                    y += part[w][set][rr][col];
+                    if (FORM == SWIGLU) u += part[w][1][rr][col];
                 }
-                a *= 512.0f;
-                u *= 512.0f;
-                reinterpret_cast<__nv_bfloat16 *>(p.out)[orow * p.ld_out + n] = __float2bfloat16_rn(silu(a) * u);
-            } else {
-                float y = 0.0f;
-#pragma unroll
-                for (int w = 0; w < WARPS; ++w) y += part[w][rr][col];
-                reinterpret_cast<float *>(p.out)[orow * p.ld_out + n] = 512.0f * y;
+                if (FORM == SWIGLU)
+                    reinterpret_cast<__nv_bfloat16 *>(p.out)[orow * p.ld_out + n] = __float2bfloat16_rn(silu(y) * u);
+                else
+                    reinterpret_cast<float *>(p.out)[orow * p.ld_out + n] = y;
             }
         }
     }
 }
+
+// COMBINE: blockIdx.x a token, its (expert, chunk) pairs dealt to the warps in
+// order; one launch, nothing shared between tokens.
+__global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv_combine(const Params p)
+{
+    extern __shared__ __align__(16) uint8_t dyn[];
+    Slot<1> *ring = reinterpret_cast<Slot<1> *>(dyn) + (threadIdx.x >> 5) * DEPTH;
+    __shared__ float part[WARPS][ROWS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int tile = blockIdx.y;
+    const int chunks = (int)((p.K + 127) / 128);
+    const bool dense = p.idx == nullptr;
+    float tot[2] = {0, 0};
+    const int units = p.k_r * chunks;
+    const int per = (units + WARPS - 1) / WARPS;
+    int u = warp * per;
+    const int u_end = min(u + per, units);
+    while (u < u_end) {
+        const int j = u / chunks, ch = u - j * chunks;
+        const int ch_end = min(chunks, ch + (u_end - u));
+        const int64_t pair = (int64_t)blockIdx.x * p.k_r + j;
+        const int e = dense ? 0 : p.idx[pair];
+        if (e >= 0 && e < p.E) {
+            const Set l[1] = {set_of(p, e, tile, 0, p.N)};
+            float acc[1][4] = {{0, 0, 0, 0}};
+            dot_range<1>(ring, l, g == 0 ? p.x + pair * p.ldx + 32 * t : nullptr, ch, 1, ch_end, p.K, acc);
+            const float coef = 512.0f * (p.gate ? p.gate[pair] * p.s_t[e] : p.s_t[e]);
+            tot[0] += coef * acc[0][0];                          // column 0 is lane t = 0's
+            tot[1] += coef * acc[0][2];
+        }
+        u += ch_end - ch;
+    }
+    if (t == 0) {
+        part[warp][g] = tot[0];
+        part[warp][g + 8] = tot[1];
+    }
+    __syncthreads();
+    if (threadIdx.x < ROWS) {
+        const int64_t n = tile_row(tile, threadIdx.x);
+        if (n < p.N) {
+            float y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WARPS; ++w) y += part[w][threadIdx.x];
+            reinterpret_cast<float *>(p.out)[(int64_t)blockIdx.x * p.ld_out + n] = y;
+        }
+    }
+}
+
+// out[t, n] = sum_j gate[t, j] y[t k_r + j, n], in slot order.
+__global__ void __launch_bounds__(THREADS) k_gemv_combine(const float *__restrict__ y, const float *__restrict__ gate,
+                                                          int64_t T, int k_r, int64_t N, float *__restrict__ out,
+                                                          int64_t ld_out)
+{
+    const int64_t n = (int64_t)blockIdx.x * THREADS + threadIdx.x;
+    const int64_t t = blockIdx.y;
+    if (n >= N) return;
+    float s = 0.0f;
+    for (int j = 0; j < k_r; ++j) s += (gate ? gate[t * k_r + j] : 1.0f) * y[(t * k_r + j) * N + n];
+    out[t * ld_out + n] = s;
+}
+
+// Opt the kernel in to its ring's shared memory (once per device).
+template <auto KERNEL>
+static nvfp4_status allow_ring(size_t bytes)
+{
+    static std::once_flag once[64];
+    static cudaError_t err[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("k_nvfp4_gemv: device");
+    std::call_once(once[dev], [&] { err[dev] = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
+    if (err[dev] != cudaSuccess) return set_error(NVFP4_ERR_CUDA, "k_nvfp4_gemv: smem attribute: %s", cudaGetErrorString(err[dev]));
+    return NVFP4_OK;
+}
+
+// Column splits of a row pair: the fewest that give two blocks per SM (or one
+// chunk of 128 columns per warp).
+static int column_splits(int64_t units, int64_t row_pairs, int64_t K)
+{
+    int s = 1;
+    while (s < WARPS && units * row_pairs * s < (int64_t)num_sms() * 2 * WARPS && (int64_t)s * 128 < K) s *= 2;
+    return s;
+}
+
+// The combine form shares weights between tokens (partial rows in the
+// workspace, a second launch) when the tokens name experts more than once.
+static bool grouped_combine(int64_t T, int32_t E, int32_t k_r) { return T > 1 && T * k_r > E / 4; }
 
 }  // namespace gemv
 }  // namespace nvfp4
 
 using namespace nvfp4;
 
+extern "C" size_t moe_nvfp4_gemv_workspace_size(int64_t T, int64_t N, int32_t E, int32_t k_r, int32_t epilogue)
+{
+    using namespace nvfp4::gemv;
+    if (T <= 0 || N <= 0 || E <= 0 || k_r <= 0 || epilogue != MOE_EPI_COMBINE_F32 || !grouped_combine(T, E, k_r)) return 0;
+    return (size_t)std::min<int64_t>(T, MAX_PAIRS / k_r) * (size_t)k_r * (size_t)N * 4;
+}
+
 extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx, const uint8_t *codes_dev,
                                        const uint8_t *scales_dev, const float *s_t_dev, int64_t N, int64_t K,
                                        int32_t E, const int32_t *expert_idx_dev, int32_t k_r, int32_t epilogue,
-                                       const float *gate_dev, void *out_dev, int64_t ld_out, void *stream)
+                                       const float *gate_dev, void *out_dev, int64_t ld_out, void *workspace,
+                                       size_t workspace_bytes, void *stream)
 {
     using namespace nvfp4::gemv;
     NVFP4_REQUIRE(epilogue == MOE_EPI_STORE_F32 || epilogue == MOE_EPI_SWIGLU_BF16 || epilogue == MOE_EPI_COMBINE_F32,
@@ -295,8 +443,8 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
                   "moe_nvfp4_gemv: need E >= 1 and 1 <= k_r <= 32");
     NVFP4_REQUIRE(expert_idx_dev || (k_r == 1 && E == 1), NVFP4_ERR_INVALID_ARG,
                   "moe_nvfp4_gemv: without expert_idx there is one weight (E = 1, k_r = 1)");
-    NVFP4_REQUIRE(N >= 1 && K >= 64 && K % 64 == 0 && K < (1ll << 31), NVFP4_ERR_UNSUPPORTED_SHAPE,
-                  "moe_nvfp4_gemv: N must be positive and K a positive multiple of 64 (N=%lld, K=%lld)", (long long)N,
+    NVFP4_REQUIRE(N >= 1 && K >= 64 && K % 64 == 0 && K < (1ll << 24), NVFP4_ERR_UNSUPPORTED_SHAPE,
+                  "moe_nvfp4_gemv: N must be positive and K a positive multiple of 64 below 2^24 (N=%lld, K=%lld)", (long long)N,
                   (long long)K);
     NVFP4_REQUIRE(epilogue != MOE_EPI_SWIGLU_BF16 || N % 2 == 0, NVFP4_ERR_UNSUPPORTED_SHAPE,
                   "moe_nvfp4_gemv: SwiGLU needs an even N");
@@ -311,26 +459,59 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
                   "moe_nvfp4_gemv: ldx must be >= K and a multiple of 8, ld_out >= the output width");
     NVFP4_REQUIRE(aligned16(x_dev) && aligned16(codes_dev) && aligned16(scales_dev), NVFP4_ERR_ALIGNMENT,
                   "moe_nvfp4_gemv: pointers must be 16-byte aligned");
-    Params p;
-    p.x = reinterpret_cast<const __nv_bfloat16 *>(x_dev);
-    p.ldx = ldx;
-    p.codes = codes_dev;
-    p.scales = scales_dev;
-    p.s_t = s_t_dev;
-    p.N = N;
-    p.K = K;
-    p.E = E;
-    p.idx = expert_idx_dev;
-    p.T = T;
-    p.k_r = k_r;
-    p.gate = gate_dev;
-    p.out = out_dev;
-    p.ld_out = ld_out;
-    const int64_t units = epilogue == MOE_EPI_COMBINE_F32 ? T : expert_idx_dev ? T * k_r : (T + COLS - 1) / COLS;
-    const dim3 grid((unsigned)units, (unsigned)tiles);
+    const size_t need = moe_nvfp4_gemv_workspace_size(T, N, E, k_r, epilogue);
+    NVFP4_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && aligned16(workspace)), NVFP4_ERR_WORKSPACE,
+                  "moe_nvfp4_gemv: workspace of %zu bytes required", need);
     cudaStream_t st = (cudaStream_t)stream;
-    if (epilogue == MOE_EPI_SWIGLU_BF16) k_nvfp4_gemv<SWIGLU><<<grid, THREADS, 0, st>>>(p);
-    else if (epilogue == MOE_EPI_COMBINE_F32) k_nvfp4_gemv<COMBINE><<<grid, THREADS, 0, st>>>(p);
-    else k_nvfp4_gemv<STORE><<<grid, THREADS, 0, st>>>(p);
-    return check_launch("k_nvfp4_gemv");
+    const bool combine = epilogue == MOE_EPI_COMBINE_F32, dense = expert_idx_dev == nullptr;
+    // the pair list holds MAX_PAIRS: longer batches run in slices of tokens
+    const int64_t slice = MAX_PAIRS / k_r;
+    const int64_t x_rows = combine ? k_r : 1;                   // rows of x per token
+    for (int64_t t0 = 0; t0 < T; t0 += slice) {
+        const int64_t tn = std::min(slice, T - t0);
+        Params p;
+        p.x = reinterpret_cast<const __nv_bfloat16 *>(x_dev) + t0 * x_rows * ldx;
+        p.ldx = ldx;
+        p.codes = codes_dev;
+        p.scales = scales_dev;
+        p.s_t = s_t_dev;
+        p.N = N;
+        p.K = K;
+        p.E = E;
+        p.idx = dense ? nullptr : expert_idx_dev + t0 * k_r;
+        p.pairs = (int)(tn * k_r);
+        p.k_r = k_r;
+        p.x_div = combine ? 1 : k_r;
+        p.gate = gate_dev ? gate_dev + t0 * k_r : nullptr;
+        p.out = epilogue == MOE_EPI_SWIGLU_BF16
+                    ? (void *)(reinterpret_cast<__nv_bfloat16 *>(out_dev) + t0 * k_r * ld_out)
+                    : (void *)(reinterpret_cast<float *>(out_dev) + (combine ? t0 : t0 * k_r) * ld_out);
+        p.ld_out = ld_out;
+        const int64_t units = dense ? (tn + COLS - 1) / COLS : tn * k_r;
+        const int64_t row_pairs = epilogue == MOE_EPI_SWIGLU_BF16 ? tiles : tiles / 2;
+        const int splits = column_splits(units, row_pairs, K);
+        const dim3 per_pair((unsigned)units, (unsigned)((row_pairs * splits + WARPS - 1) / WARPS));
+        constexpr size_t RING1 = sizeof(Slot<1>) * DEPTH * WARPS, RING2 = sizeof(Slot<2>) * DEPTH * WARPS;
+        nvfp4_status rc = combine && need == 0 ? allow_ring<k_nvfp4_gemv_combine>(RING1)
+                          : epilogue == MOE_EPI_SWIGLU_BF16 ? allow_ring<k_nvfp4_gemv<SWIGLU>>(RING2)
+                                                            : allow_ring<k_nvfp4_gemv<STORE>>(RING2);
+        if (rc != NVFP4_OK) return rc;
+        if (combine && need == 0) {
+            k_nvfp4_gemv_combine<<<dim3((unsigned)tn, (unsigned)tiles), THREADS, RING1, st>>>(p);
+        } else if (combine) {
+            float *out = reinterpret_cast<float *>(p.out);
+            p.out = workspace;
+            p.ld_out = N;
+            k_nvfp4_gemv<STORE><<<per_pair, THREADS, RING2, st>>>(p, splits);
+            if (check_launch("k_nvfp4_gemv") != NVFP4_OK) return NVFP4_ERR_CUDA;
+            k_gemv_combine<<<dim3((unsigned)((N + THREADS - 1) / THREADS), (unsigned)tn), THREADS, 0, st>>>(
+                reinterpret_cast<const float *>(workspace), p.gate, tn, k_r, N, out, ld_out);
+        } else if (epilogue == MOE_EPI_SWIGLU_BF16) {
+            k_nvfp4_gemv<SWIGLU><<<per_pair, THREADS, RING2, st>>>(p, splits);
+        } else {
+            k_nvfp4_gemv<STORE><<<per_pair, THREADS, RING2, st>>>(p, splits);
+        }
+        if (check_launch("k_nvfp4_gemv") != NVFP4_OK) return NVFP4_ERR_CUDA;
+    }
+    return NVFP4_OK;
 }

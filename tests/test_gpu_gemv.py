@@ -38,6 +38,17 @@ def bound(K, x, w):
     return sum_bound(K + 8, torch.bmm(w.abs(), x.abs()[:, :, None])[:, :, 0])
 
 
+def check_swiglu(h, y, b):
+    """h against the SwiGLU of y = [gate | up], known to b."""
+    n = y.shape[1] // 2
+    a, u, ba, bu = y[:, :n], y[:, n:], b[:, :n], b[:, n:]
+    sig = torch.sigmoid(a)
+    want = a * sig * u
+    # d silu / da <= 1.1; f32 sigmoid as in the SwiGLU tests
+    lim = 1.1 * ba * (u.abs() + bu) + (a * sig).abs() * bu + (16 + a.abs()) * 2.0 ** -23 * want.abs()
+    check(h, want, 1.01 * lim + rounding(BF16, want.abs() + lim))
+
+
 @pytest.mark.parametrize("T,E,kr", [(1, 8, 2), (1, 5, 1), (3, 16, 8), (9, 4, 3)])
 @pytest.mark.parametrize("N,K", [(16, 64), (130, 128), (256, 192), (1536, 2048), (34, 704)])
 def test_store_and_swiglu(cuda, T, E, kr, N, K):
@@ -51,13 +62,7 @@ def test_store_and_swiglu(cuda, T, E, kr, N, K):
     got = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx)
     check(got, y, b + rounding(F32, y))
     h = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_SWIGLU_BF16)
-    a, u = y[:, : N // 2], y[:, N // 2:]
-    ba, bu = b[:, : N // 2], b[:, N // 2:]
-    sig = torch.sigmoid(a)
-    want = a * sig * u
-    # d silu / da <= 1.1; f32 sigmoid as in the SwiGLU tests
-    lim = 1.1 * ba * (u.abs() + bu) + (a * sig).abs() * bu + (16 + a.abs()) * 2.0 ** -23 * want.abs()
-    check(h, want, 1.01 * lim + rounding(BF16, want.abs() + lim))
+    check_swiglu(h, y, b)
 
 
 @pytest.mark.parametrize("T,E,kr", [(1, 8, 8), (2, 5, 1), (16, 32, 8), (5, 4, 3)])
@@ -88,10 +93,31 @@ def test_dense(cuda, T, N, K):
     check(got, y, sum_bound(K + 8, x.double().abs() @ w[0].abs().t()) + rounding(F32, y))
     if N % 2 == 0:
         h = api.nvfp4_gemv(x, codes, sf, s, N, K, epilogue=api.EPI_SWIGLU_BF16)
+        b = sum_bound(K + 8, x.double().abs() @ w[0].abs().t())
+        check_swiglu(h, y, b)
         idx = torch.zeros(T, 1, dtype=I32, device=cuda)
-        assert torch.equal(h, api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_SWIGLU_BF16))
+        check_swiglu(api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_SWIGLU_BF16), y, b)
     c = api.nvfp4_gemv(x, codes, sf, s, N, K, epilogue=api.EPI_COMBINE_F32)
     check(c, y, sum_bound(K + 8, x.double().abs() @ w[0].abs().t()) + rounding(F32, y))
+
+
+def test_many_tokens_share_experts(cuda):
+    """More pairs than one launch lists, more tokens per expert than one pass."""
+    T, E, kr, N, K = 300, 5, 4, 48, 192
+    codes, sf, s, w = weights(20, E, N, K)
+    x = rnd(21, T, K)
+    idx = torch.randint(-1, E, (T, kr), generator=torch.Generator().manual_seed(22)).to(I32).to(cuda)
+    flat = idx.view(-1).long()
+    live = (flat >= 0).double()[:, None]
+    wf = w[flat.clamp_min(0)]
+    xr = x.double().repeat_interleave(kr, 0)
+    y = torch.bmm(wf, xr[:, :, None])[:, :, 0] * live
+    check(api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx), y, bound(K, xr, wf) * live + rounding(F32, y))
+    xc = rnd(23, T * kr, K)
+    y = torch.bmm(wf, xc.double()[:, :, None])[:, :, 0] * live
+    got = api.nvfp4_gemv(xc, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_COMBINE_F32)
+    want = y.view(T, kr, N).sum(1)
+    check(got, want, (bound(K + kr, xc.double(), wf) * live).view(T, kr, N).sum(1) + rounding(F32, want))
 
 
 def test_every_code_and_scale_decodes_exactly(cuda):

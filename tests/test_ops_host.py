@@ -108,13 +108,20 @@ def test_combine_and_route_backward():
 
 
 def test_gemv():
-    #       x     T  ldx   codes sc    s_t   N    K    E  idx  kr epi gate  out   ld  stream
-    good = [FAKE, 2, 128, FAKE, FAKE, FAKE, 256, 128, 8, FAKE, 2, 0, None, FAKE, 256, None]
+    #       x     T  ldx   codes sc    s_t   N    K    E  idx  kr epi gate  out   ld  ws    n  stream
+    good = [FAKE, 2, 128, FAKE, FAKE, FAKE, 256, 128, 8, FAKE, 2, 0, None, FAKE, 256, None, 0, None]
     calls("moe_nvfp4_gemv", good, [
         (0, None, INVALID), (3, None, INVALID), (4, None, INVALID), (5, None, INVALID), (13, None, INVALID),
         (9, None, INVALID), (11, 2, INVALID), (11, 4, INVALID), (1, -1, INVALID), (7, 96, SHAPE), (7, 0, SHAPE),
         (6, 0, SHAPE), (8, 0, SHAPE), (10, 0, SHAPE), (10, 33, SHAPE), (2, 120, ALIGN), (2, 132, ALIGN),
         (14, 255, ALIGN), (0, ODD, ALIGN), (3, ODD, ALIGN), (4, ODD, ALIGN)])
+    many = list(good)
+    many[1], many[11] = 16, api.EPI_COMBINE_F32            # tokens share experts: a workspace is required
+    need = _lib.load().moe_nvfp4_gemv_workspace_size(16, 256, 8, 2, api.EPI_COMBINE_F32)
+    assert need == 16 * 2 * 256 * 4 and _lib.load().moe_nvfp4_gemv_workspace_size(1, 256, 8, 2, 3) == 0
+    calls("moe_nvfp4_gemv", many, [(15, None, WORKSPACE), (15, ODD, WORKSPACE)])
+    many[15], many[16] = FAKE, need - 1
+    assert _lib.load().moe_nvfp4_gemv(*many) == WORKSPACE
     odd = list(good)
     odd[6], odd[11] = 257, 1
     assert _lib.load().moe_nvfp4_gemv(*odd) == SHAPE
@@ -145,20 +152,30 @@ def test_binding_refuses_host_tensors():
 
 
 def test_binding_checks_operands():
-    dev = torch.device("cpu")
-    t = torch.zeros(4, 8)
+    t = torch.zeros(4, 8)                                    # a host tensor: device index -1
+    assert api._matrix(t, "x", torch.float32, 4, 8, -1) == 8
+    assert api._matrix(t[:1, :5], "x", torch.float32, None, 5, -1) == 16      # one row: no stride of its own
     with pytest.raises(ValueError, match="need torch.bfloat16"):
-        api._matrix(t, "x", torch.bfloat16, 4, 8, dev)
+        api._matrix(t, "x", torch.bfloat16, 4, 8, -1)
     with pytest.raises(ValueError, match="need"):
-        api._matrix(t, "x", torch.float32, 4, 9, dev)
+        api._matrix(t, "x", torch.float32, 4, 9, -1)
     with pytest.raises(ValueError, match="need"):
-        api._matrix(t, "x", torch.float32, 3, 8, dev)
+        api._matrix(t, "x", torch.float32, 3, 8, -1)
+    with pytest.raises(ValueError, match="need"):
+        api._matrix(t.view(2, 2, 8), "x", torch.float32, 2, 2, -1)
     with pytest.raises(ValueError, match="contiguous"):
-        api._matrix(t.t(), "x", torch.float32, 8, 4, dev)
-    with pytest.raises(ValueError, match="expected"):
-        api._matrix(t, "x", torch.float32, 4, 8, torch.device("meta"))
+        api._matrix(t.t(), "x", torch.float32, 8, 4, -1)
+    with pytest.raises(ValueError, match="expected cuda:0"):
+        api._matrix(t, "x", torch.float32, 4, 8, 0)
     with pytest.raises(ValueError, match="elements"):
-        api._vector(t, "x", torch.float32, 31, dev)
+        api._vector(t, "x", torch.float32, 31, -1)
+    with pytest.raises(ValueError, match="elements"):
+        api._vector(t.t(), "x", torch.float32, 32, -1)
+    with pytest.raises(ValueError, match="expected cuda:0"):
+        api._vector(t, "x", torch.float32, 32, 0)
     u8 = torch.zeros(4, 160, dtype=torch.uint8)
+    assert api._act8(api.Act8(u8, u8[:, :8]), "x", 4, 160, -1) == (160, 160)
     with pytest.raises(ValueError, match="scales"):
-        api._act8(api.Act8(u8, u8[:, :4]), "x", 4, 160, dev)
+        api._act8(api.Act8(u8, u8[:, :4]), "x", 4, 160, -1)
+    with pytest.raises(ValueError, match="scales"):
+        api._act8(api.Act8(u8, u8[:3, :8]), "x", 4, 160, -1)
