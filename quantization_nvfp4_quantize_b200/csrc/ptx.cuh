@@ -407,6 +407,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar)
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
+// The same without releasing earlier writes: for handing on what only tcgen05
+// accesses touched (ordered by tc_fence_before).  A release at cluster scope
+// would first wait for every global store this thread has in flight.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_bar)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+}
+
 // 2D tiled TMA load into this CTA's shared memory whose completion is
 // counted on an mbarrier in the pair's leader CTA (cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *m, int32_t x, int32_t y,

@@ -568,7 +568,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     // the accumulator is free once both CTAs' warps have read it
                     ptx::tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
+                    if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
                 }
                 if (!ok) break;
                 const int acc = iter & 1;
@@ -595,7 +595,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                         if (c == 3) {
                             ptx::tc_fence_before();
                             __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
+                            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
                         }
                     }
                     store_rows<ADD>(p, reinterpret_cast<OutT *>(p.out), row + c * 32, rows - c * 32, m, y);
@@ -618,7 +618,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     if (c + 32 >= half_n) {
                         ptx::tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
+                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
                     }
                     const int64_t r = w.n0 + half * half_n + c;
                     const int rows = (int)(w.n_end - r);
