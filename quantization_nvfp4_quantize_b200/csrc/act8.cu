@@ -22,6 +22,7 @@ namespace nvfp4 {
 namespace act8 {
 
 constexpr int THREADS = 256;
+constexpr int QUANT_BLOCKS = 6, SWIGLU_BLOCKS = 5, DEQUANT_BLOCKS = 8, BACKWARD_BLOCKS = 4;     // resident per SM
 
 // p + 127 of a group from the largest |x| (bf16 bits); 255 for Inf / NaN.
 __device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits)
@@ -107,7 +108,7 @@ __device__ __forceinline__ void store16(uint8_t *row, int64_t c, int64_t K, uint
 // padding of the scale row is written too).  Consecutive lanes take
 // consecutive items; the two lanes of a group always sit side by side because
 // `items` and the stride are even.
-__global__ void __launch_bounds__(THREADS) k_act8_quantize(const __nv_bfloat16 *__restrict__ x, int64_t M, int64_t K,
+__global__ void __launch_bounds__(THREADS, QUANT_BLOCKS) k_act8_quantize(const __nv_bfloat16 *__restrict__ x, int64_t M, int64_t K,
                                                            int64_t ldx, uint8_t *__restrict__ codes, int64_t ldc,
                                                            uint8_t *__restrict__ scales, int64_t lds, int items)
 {
@@ -149,7 +150,7 @@ __device__ __forceinline__ void decode4(uint32_t w, float v[4])
 // One item = 16 columns, as in the quantizer.  Every kept value is exact in
 // bf16.  Row r of the result is kept row src_rows[r] (null: r); an index
 // outside [0, T) gives zeros.
-__global__ void __launch_bounds__(THREADS) k_act8_dequantize(const uint8_t *__restrict__ codes, int64_t ldc,
+__global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(const uint8_t *__restrict__ codes, int64_t ldc,
                                                              const uint8_t *__restrict__ scales, int64_t lds,
                                                              const int32_t *__restrict__ src_rows, int64_t T,
                                                              int64_t M, int64_t K, __nv_bfloat16 *__restrict__ x,
@@ -201,12 +202,24 @@ __global__ void __launch_bounds__(THREADS) k_act8_dequantize(const uint8_t *__re
     }
 }
 
-// 1 / (1 + e^-a); e^-a may be infinite (the quotient is then 0).
-__device__ __forceinline__ float sigmoid(float a) { return __fdividef(1.0f, 1.0f + expf(-a)); }
+// 1 / (1 + 2^(-a log2 e)) of two values; the power may be infinite (the
+// quotient is then 0).  Error: the exponent's rounding, |a| 2^-24 relative, and
+// a few units in the last place.
+__device__ __forceinline__ float2 sigmoid2(float2 a)
+{
+    const float2 e = __fmul2_rn(a, make_float2(-1.44269504f, -1.44269504f));
+    float x, y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(x) : "f"(e.x));
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(e.y));
+    const float2 d = __fadd2_rn(make_float2(x, y), make_float2(1.0f, 1.0f));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(x) : "f"(d.x));
+    asm("rcp.approx.f32 %0, %1;" : "=f"(y) : "f"(d.y));
+    return make_float2(x, y);
+}
 
 // h = silu(gate) * up and both inputs kept: one item = 16 columns of gate and
 // the same 16 of up.
-__global__ void __launch_bounds__(THREADS) k_swiglu_act8(const __nv_bfloat16 *__restrict__ y, int64_t M, int64_t I,
+__global__ void __launch_bounds__(THREADS, SWIGLU_BLOCKS) k_swiglu_act8(const __nv_bfloat16 *__restrict__ y, int64_t M, int64_t I,
                                                          int64_t ldy, __nv_bfloat16 *__restrict__ h, int64_t ldh,
                                                          uint8_t *__restrict__ codes, int64_t ldc,
                                                          uint8_t *__restrict__ scales, int64_t lds, int items,
@@ -240,8 +253,9 @@ __global__ void __launch_bounds__(THREADS) k_swiglu_act8(const __nv_bfloat16 *__
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float a0 = bf16lo(a[i]), a1 = bf16hi(a[i]);
-                o[i] = pack_bf16(a0 * sigmoid(a0) * bf16lo(b[i]), a1 * sigmoid(a1) * bf16hi(b[i]));
+                const float2 av = make_float2(bf16lo(a[i]), bf16hi(a[i]));
+                const float2 hv = __fmul2_rn(__fmul2_rn(av, sigmoid2(av)), make_float2(bf16lo(b[i]), bf16hi(b[i])));
+                o[i] = pack_bf16(hv.x, hv.y);
             }
             uint4 *dst = reinterpret_cast<uint4 *>(h + row * ldh + c);
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -259,7 +273,7 @@ __global__ void __launch_bounds__(THREADS) k_swiglu_act8(const __nv_bfloat16 *__
 // w the row's router weight.  One warp per row, 8 columns per lane and step;
 // the row sum is a lane-ordered f32 sum and a fixed shuffle tree, so it does
 // not change from run to run.
-__global__ void __launch_bounds__(THREADS) k_swiglu_act8_backward(
+__global__ void __launch_bounds__(THREADS, BACKWARD_BLOCKS) k_swiglu_act8_backward(
     const uint8_t *__restrict__ codes, int64_t ldc, const uint8_t *__restrict__ scales, int64_t lds,
     const __nv_bfloat16 *__restrict__ dh, int64_t lddh, const float *__restrict__ row_gate, int64_t M, int64_t I,
     __nv_bfloat16 *__restrict__ dy, int64_t lddy, __nv_bfloat16 *__restrict__ gh, int64_t ldgh,
@@ -271,7 +285,8 @@ __global__ void __launch_bounds__(THREADS) k_swiglu_act8_backward(
         const uint8_t *crow = codes + row * ldc;
         const uint8_t *srow = scales + row * lds;
         const float w = row_gate ? row_gate[row] : 1.0f;
-        float sum = 0.0f;
+        const float2 w2 = make_float2(w, w);
+        float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll 3
         for (int64_t c = lane * 8; c < I; c += 256) {
             const uint2 ca = *reinterpret_cast<const uint2 *>(crow + c);
@@ -285,30 +300,29 @@ __global__ void __launch_bounds__(THREADS) k_swiglu_act8_backward(
             decode4(cb.x, b);
             decode4(cb.y, b + 4);
             uint32_t oa[4], ob[4], oh[4];
+            const float2 fa2 = make_float2(fa, fa), fb2 = make_float2(fb, fb), one = make_float2(1.0f, 1.0f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float da[2], db[2], hh[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float av = a[2 * i + j] * fa, bv = b[2 * i + j] * fb;
-                    const float u = j ? bf16hi(d[i]) : bf16lo(d[i]);
-                    const float s = sigmoid(av), as = av * s, h = as * bv, g = w * u;
-                    sum += u * h;
-                    da[j] = g * bv * s * (1.0f + av * (1.0f - s));
-                    db[j] = g * as;
-                    hh[j] = w * h;
-                }
-                oa[i] = pack_bf16(da[0], da[1]);
-                ob[i] = pack_bf16(db[0], db[1]);
-                oh[i] = pack_bf16(hh[0], hh[1]);
+                const float2 av = __fmul2_rn(make_float2(a[2 * i], a[2 * i + 1]), fa2);
+                const float2 bv = __fmul2_rn(make_float2(b[2 * i], b[2 * i + 1]), fb2);
+                const float2 u = make_float2(bf16lo(d[i]), bf16hi(d[i]));
+                const float2 s = sigmoid2(av), as = __fmul2_rn(av, s), h = __fmul2_rn(as, bv), g = __fmul2_rn(w2, u);
+                sum = __ffma2_rn(u, h, sum);
+                const float2 t = __ffma2_rn(av, __ffma2_rn(s, make_float2(-1.0f, -1.0f), one), one);
+                const float2 da = __fmul2_rn(__fmul2_rn(__fmul2_rn(g, bv), s), t);
+                const float2 db = __fmul2_rn(g, as), hw = __fmul2_rn(w2, h);
+                oa[i] = pack_bf16(da.x, da.y);
+                ob[i] = pack_bf16(db.x, db.y);
+                oh[i] = pack_bf16(hw.x, hw.y);
             }
             *reinterpret_cast<uint4 *>(dy + row * lddy + c) = make_uint4(oa[0], oa[1], oa[2], oa[3]);
             *reinterpret_cast<uint4 *>(dy + row * lddy + I + c) = make_uint4(ob[0], ob[1], ob[2], ob[3]);
             if (gh) *reinterpret_cast<uint4 *>(gh + row * ldgh + c) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
         }
+        float total = sum.x + sum.y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (dgate && lane == 0) dgate[row] = sum;
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        if (dgate && lane == 0) dgate[row] = total;
     }
 }
 
@@ -376,11 +390,13 @@ __global__ void __launch_bounds__(THREADS) k_route_backward(const int32_t *__res
     }
 }
 
-// Blocks of a streaming kernel: `work` items, at most 8 resident blocks of
-// 256 threads per SM (more only adds block launches).
-static unsigned stream_blocks(int64_t work)
+// Blocks of a streaming kernel over `work` threads: at most the `resident`
+// ones per SM that its registers allow, so that no second wave of blocks
+// starts when the first has shared out all the work (8 per SM where 6 fit:
+// 45 instead of 37 us for 16384 x 4096).
+static unsigned stream_blocks(int64_t work, int resident)
 {
-    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((work + THREADS - 1) / THREADS, (int64_t)num_sms() * 8));
+    return (unsigned)std::max<int64_t>(1, std::min<int64_t>((work + THREADS - 1) / THREADS, (int64_t)num_sms() * resident));
 }
 
 }  // namespace act8
@@ -389,7 +405,7 @@ nvfp4_status act8_expand(const uint8_t *codes, int64_t ldc, const uint8_t *scale
                          int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, cudaStream_t stream)
 {
     const int items = (int)((K + 15) / 16);
-    act8::k_act8_dequantize<<<act8::stream_blocks(M * items), act8::THREADS, 0, stream>>>(
+    act8::k_act8_dequantize<<<act8::stream_blocks(M * items, act8::DEQUANT_BLOCKS), act8::THREADS, 0, stream>>>(
         codes, ldc, scales, lds, rows, T, M, K, reinterpret_cast<__nv_bfloat16 *>(x), ldx, items);
     return check_launch("k_act8_dequantize");
 }
@@ -415,7 +431,7 @@ extern "C" nvfp4_status act8_quantize(const void *x_dev, int64_t M, int64_t K, i
     NVFP4_REQUIRE(aligned16(x_dev) && aligned16(codes_dev) && aligned16(scales_dev), NVFP4_ERR_ALIGNMENT,
                   "act8_quantize: pointers must be 16-byte aligned");
     const int items = (int)((K + 127) / 128 * 8);
-    k_act8_quantize<<<stream_blocks(M * items), THREADS, 0, (cudaStream_t)stream>>>(
+    k_act8_quantize<<<stream_blocks(M * items, QUANT_BLOCKS), THREADS, 0, (cudaStream_t)stream>>>(
         reinterpret_cast<const __nv_bfloat16 *>(x_dev), M, K, ldx, codes_dev, ld_codes, scales_dev, ld_scales, items);
     return check_launch("k_act8_quantize");
 }
@@ -457,7 +473,7 @@ extern "C" nvfp4_status moe_swiglu_act8(const void *y_dev, int64_t M, int64_t I,
     NVFP4_REQUIRE(aligned16(y_dev) && aligned16(h_dev) && aligned16(codes_dev) && aligned16(scales_dev),
                   NVFP4_ERR_ALIGNMENT, "moe_swiglu_act8: pointers must be 16-byte aligned");
     const int items = (int)(I / 16);
-    k_swiglu_act8<<<stream_blocks(M * items), THREADS, 0, (cudaStream_t)stream>>>(
+    k_swiglu_act8<<<stream_blocks(M * items, SWIGLU_BLOCKS), THREADS, 0, (cudaStream_t)stream>>>(
         reinterpret_cast<const __nv_bfloat16 *>(y_dev), M, I, ldy, reinterpret_cast<__nv_bfloat16 *>(h_dev), ldh,
         codes_dev, ld_codes, scales_dev, ld_scales, items, (int)(row_bytes - 2 * I / 32));
     return check_launch("k_swiglu_act8");
@@ -488,9 +504,7 @@ extern "C" nvfp4_status moe_swiglu_act8_backward(const uint8_t *codes_dev, int64
                   "moe_swiglu_act8_backward: lddh >= I, lddy >= 2I, ldgh >= I, multiples of 8");
     NVFP4_REQUIRE(aligned16(codes_dev) && aligned16(dh_dev) && aligned16(dy_dev) && aligned16(gh_dev),
                   NVFP4_ERR_ALIGNMENT, "moe_swiglu_act8_backward: pointers must be 16-byte aligned");
-    const int64_t rows_per_block = THREADS / 32;
-    const unsigned blocks = (unsigned)std::min<int64_t>((M + rows_per_block - 1) / rows_per_block,
-                                                        (int64_t)num_sms() * 8);
+    const unsigned blocks = stream_blocks(M * 32, BACKWARD_BLOCKS);          // a warp per row
     k_swiglu_act8_backward<<<blocks, THREADS, 0, (cudaStream_t)stream>>>(
         codes_dev, ld_codes, scales_dev, ld_scales, reinterpret_cast<const __nv_bfloat16 *>(dh_dev), lddh, row_gate_dev,
         M, I, reinterpret_cast<__nv_bfloat16 *>(dy_dev), lddy, reinterpret_cast<__nv_bfloat16 *>(gh_dev), ldgh,
