@@ -22,8 +22,8 @@
 // long as both operands agree, so each lane feeds its own 32 columns and x is
 // loaded in the same arrangement.  The 16 rows are 4 rows of each 32-row
 // quarter of a 128-row scale atom: their scales are 64 contiguous bytes.
-// A block's 8 warps split the columns (or the token's experts); partial sums
-// meet in shared memory and are added in warp order.
+// Warps that split the columns (or a token's experts) meet in shared memory;
+// their sums are added in warp order.
 #include "common.cuh"
 
 #include <algorithm>
@@ -32,11 +32,13 @@
 namespace nvfp4 {
 namespace gemv {
 
-constexpr int WARPS = 8;
+constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
-constexpr int ROWS = 16;                 // weight rows per warp tile
+constexpr int COMBINE_WARPS = 8;         // of a one-launch combine block
+constexpr int ROWS = 16;                 // weight rows of a set
 constexpr int COLS = 8;                  // tokens per MMA
 
+constexpr int BLOCKS = 4;                // resident per SM
 constexpr int DEPTH = 4;                 // ring slots per warp: one chunk computed, DEPTH - 1 in flight
 constexpr int MAX_PAIRS = 1024;          // (token, slot) pairs per launch
 
@@ -239,13 +241,13 @@ __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + exp
 
 // STORE and SWIGLU.  A warp takes two 16-row sets (STORE: 32 output rows;
 // SWIGLU: 16 gate rows and their up rows) and one of `splits` interleaved
-// parts of the columns; a block's 8 warps are 8 / splits such row pairs.
+// parts of the columns; a block's 4 warps are 4 / splits such row pairs.
 // blockIdx.x: (token, slot) pair (dense: group of 8 tokens), fastest, so that
 // blocks that share an expert's rows run together and meet in L2.  The block
 // of the first pair that names an expert serves every pair that does, 8 per
 // pass of its weights; the others leave at once.
 template <int FORM>
-__global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p, int splits)
+__global__ void __launch_bounds__(THREADS, BLOCKS) k_nvfp4_gemv(const Params p, int splits)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
     Slot<2> *ring = reinterpret_cast<Slot<2> *>(dyn) + (threadIdx.x >> 5) * DEPTH;
@@ -262,14 +264,25 @@ __global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p, int s
     const bool dense = p.idx == nullptr;
     int e = 0, members = 1, first = b;
     bool listed = false;
+    unsigned set_bits = 0;                                       // up to 32 pairs: the expert's, as bits
     if (dense) {
         first = b * COLS;
         members = min(COLS, p.pairs - first);
+    } else if (p.pairs <= 32) {
+        const int mine = lane < p.pairs ? p.idx[lane] : -1;
+        e = __shfl_sync(0xffffffffu, mine, b);
+        if (e < 0 || e >= p.E) {
+            e = -1;                                              // no such expert: zeros, for this pair alone
+        } else {
+            set_bits = __ballot_sync(0xffffffffu, mine == e);
+            if (set_bits & ((1u << b) - 1u)) return;
+            members = __popc(set_bits);
+        }
     } else {
         e = p.idx[b];
         if (e < 0 || e >= p.E) {
-            e = -1;                                              // no such expert: zeros, for this pair alone
-        } else if (p.pairs > 1) {
+            e = -1;
+        } else {
             if (warp == 0) {
                 int n = 0;
                 bool later = false;
@@ -289,6 +302,12 @@ __global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p, int s
             if (members == 0) return;
         }
     }
+    // the pair in column `col` (< members) of this block's products
+    auto pair_of = [&](int col) {
+        if (listed) return list[col];
+        if (members > 1 && set_bits) return (int)__fns(set_bits, 0, col + 1);
+        return first + col;
+    };
     // STORE: the row pair's two sets are neighbouring tiles; SWIGLU: gate and up
     const int tile0 = FORM == SWIGLU ? rp : 2 * rp, tile1 = FORM == SWIGLU ? rp : 2 * rp + 1;
     for (int m0 = 0; m0 < members; m0 += COLS) {
@@ -296,7 +315,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p, int s
         float coef = 0.0f;
         if (e >= 0) {
             const bool mine = m0 + g < members;
-            const int pair = mine ? (listed ? list[m0 + g] : first + m0 + g) : 0;
+            const int pair = mine ? pair_of(m0 + g) : 0;
             const Set l[2] = {set_of(p, e, tile0, 0, n_rows),
                               set_of(p, e, tile1, FORM == SWIGLU ? n_rows : 0, n_rows)};
             dot_range<2>(ring, l, mine ? p.x + (int64_t)(pair / p.x_div) * p.ldx + 32 * t : nullptr, split, splits, chunks, p.K, acc);
@@ -309,23 +328,29 @@ __global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p, int s
             *reinterpret_cast<float2 *>(&part[warp][i][g + 8][2 * t]) = make_float2(coef * acc[i][2], coef * acc[i][3]);
         }
         __syncthreads();
-        // one thread per (row, column of the 8) of a set, row pairs in turn
-        const int rr = threadIdx.x & 15, col = (threadIdx.x >> 4) & 7, set = threadIdx.x >> 7;
-        if (m0 + col < members && (FORM == STORE || set == 0)) {
-            const int64_t orow = listed ? list[m0 + col] : first + m0 + col;
+        // one thread per row and column; sets and row pairs in turn
+        static_assert(THREADS == ROWS * COLS, "one output per thread and set");
+        const int rr = threadIdx.x & 15, col = threadIdx.x >> 4;
+        if (m0 + col < members) {
+            const int64_t orow = pair_of(m0 + col);
             for (int j = 0; j < per_block; ++j) {
                 const int orp = (int)blockIdx.y * per_block + j;
-                const int64_t n = tile_row(FORM == SWIGLU ? orp : 2 * orp + set, rr);
-                if (n >= n_rows) continue;
-                float y = 0.0f, u = 0.0f;
+                float y[2] = {0.0f, 0.0f};
                 for (int w = j * splits; w < (j + 1) * splits; ++w) {
-                    y += part[w][set][rr][col];
-                    if (FORM == SWIGLU) u += part[w][1][rr][col];
+                    y[0] += part[w][0][rr][col];
+                    y[1] += part[w][1][rr][col];
                 }
-                if (FORM == SWIGLU)
-                    reinterpret_cast<__nv_bfloat16 *>(p.out)[orow * p.ld_out + n] = __float2bfloat16_rn(silu(y) * u);
-                else
-                    reinterpret_cast<float *>(p.out)[orow * p.ld_out + n] = y;
+                if (FORM == SWIGLU) {
+                    const int64_t n = tile_row(orp, rr);
+                    if (n < n_rows)
+                        reinterpret_cast<__nv_bfloat16 *>(p.out)[orow * p.ld_out + n] = __float2bfloat16_rn(silu(y[0]) * y[1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int64_t n = tile_row(2 * orp + i, rr);
+                        if (n < n_rows) reinterpret_cast<float *>(p.out)[orow * p.ld_out + n] = y[i];
+                    }
+                }
             }
         }
     }
@@ -333,18 +358,18 @@ __global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv(const Params p, int s
 
 // COMBINE: blockIdx.x a token, its (expert, chunk) pairs dealt to the warps in
 // order; one launch, nothing shared between tokens.
-__global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv_combine(const Params p)
+__global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(const Params p)
 {
     extern __shared__ __align__(16) uint8_t dyn[];
     Slot<1> *ring = reinterpret_cast<Slot<1> *>(dyn) + (threadIdx.x >> 5) * DEPTH;
-    __shared__ float part[WARPS][ROWS];
+    __shared__ float part[COMBINE_WARPS][ROWS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int tile = blockIdx.y;
     const int chunks = (int)((p.K + 127) / 128);
     const bool dense = p.idx == nullptr;
     float tot[2] = {0, 0};
     const int units = p.k_r * chunks;
-    const int per = (units + WARPS - 1) / WARPS;
+    const int per = (units + COMBINE_WARPS - 1) / COMBINE_WARPS;
     int u = warp * per;
     const int u_end = min(u + per, units);
     while (u < u_end) {
@@ -372,7 +397,7 @@ __global__ void __launch_bounds__(THREADS, 2) k_nvfp4_gemv_combine(const Params 
         if (n < p.N) {
             float y = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) y += part[w][threadIdx.x];
+            for (int w = 0; w < COMBINE_WARPS; ++w) y += part[w][threadIdx.x];
             reinterpret_cast<float *>(p.out)[(int64_t)blockIdx.x * p.ld_out + n] = y;
         }
     }
@@ -404,7 +429,7 @@ static nvfp4_status allow_ring(size_t bytes)
     return NVFP4_OK;
 }
 
-// Column splits of a row pair: the fewest that give two blocks per SM (or one
+// Column splits of a row pair: the fewest that give every SM two blocks (or one
 // chunk of 128 columns per warp).
 static int column_splits(int64_t units, int64_t row_pairs, int64_t K)
 {
@@ -491,13 +516,13 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
         const int64_t row_pairs = epilogue == MOE_EPI_SWIGLU_BF16 ? tiles : tiles / 2;
         const int splits = column_splits(units, row_pairs, K);
         const dim3 per_pair((unsigned)units, (unsigned)((row_pairs * splits + WARPS - 1) / WARPS));
-        constexpr size_t RING1 = sizeof(Slot<1>) * DEPTH * WARPS, RING2 = sizeof(Slot<2>) * DEPTH * WARPS;
+        constexpr size_t RING1 = sizeof(Slot<1>) * DEPTH * COMBINE_WARPS, RING2 = sizeof(Slot<2>) * DEPTH * WARPS;
         nvfp4_status rc = combine && need == 0 ? allow_ring<k_nvfp4_gemv_combine>(RING1)
                           : epilogue == MOE_EPI_SWIGLU_BF16 ? allow_ring<k_nvfp4_gemv<SWIGLU>>(RING2)
                                                             : allow_ring<k_nvfp4_gemv<STORE>>(RING2);
         if (rc != NVFP4_OK) return rc;
         if (combine && need == 0) {
-            k_nvfp4_gemv_combine<<<dim3((unsigned)tn, (unsigned)tiles), THREADS, RING1, st>>>(p);
+            k_nvfp4_gemv_combine<<<dim3((unsigned)tn, (unsigned)tiles), 32 * COMBINE_WARPS, RING1, st>>>(p);
         } else if (combine) {
             float *out = reinterpret_cast<float *>(p.out);
             p.out = workspace;
