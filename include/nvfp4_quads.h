@@ -502,11 +502,13 @@ NVFP4_API nvfp4_status moe_w8a8_grouped_gemm(
  *   w_dev        bf16 [E x N x K], contiguous.
  *   offsets_dev  int32 [E+1], ascending, in [0, M].  Bounds outside that are
  *                read as their running maximum clamped to [0, M].
- *   out_dev      f32 (out_f32 != 0) or bf16; f32 accumulation, one rounding.
+ *   out_dev      f32 (out_f32 != 0) or bf16; f32 accumulation on the tensor
+ *                core, whose additions truncate (about 1.6e-6 in norm per 1024
+ *                terms, which an f32 result shows), and one rounding to bf16.
  * Rows below offsets[0] or from offsets[E] on are neither read into a result
  * nor written.  E <= 256, K % 8 == 0, lda % 8 == 0, any N, ld_out >= the
- * output width (its rows need no alignment; 32-byte aligned ones are stored
- * fastest); a and w 16-byte aligned, out aligned to its elements.
+ * output width (any); a and w 16-byte aligned, out aligned to its elements.
+ * The reduced width must not be 0.
  *
  * moe_ragged_wgrad -- the weight gradient of the same product,
  *   out[e, n, k] = sum_{r in segment e} g[r, n] a[row(r), k]    (+ out if accumulate)
@@ -523,7 +525,8 @@ NVFP4_API nvfp4_status moe_w8a8_grouped_gemm(
  *                aligned: kept (a in 8 bits): the kept rows in bf16, gathered
  *                into row order; a small result: f32 partial results of
  *                segments split over the SMs; otherwise 0.
- * Sums run in a fixed order: the same inputs give the same bits.  E <= 256,
+ * Sums run in a fixed order: the same inputs give the same bits; at most 512
+ * rows are summed on the tensor core at a time, the parts in f32.  E <= 256,
  * ldg % 8 == 0, lda % 8 == 0 (16 for codes), ld_scales % 4 == 0, any N and K.
  *
  * Both: Inf and NaN stay in the rows (WGRAD: the segments) that hold them.

@@ -482,8 +482,10 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
                   "moe_nvfp4_gemv: null pointer");
     NVFP4_REQUIRE(ldx >= K && ldx % 8 == 0 && ld_out >= rows, NVFP4_ERR_ALIGNMENT,
                   "moe_nvfp4_gemv: ldx must be >= K and a multiple of 8, ld_out >= the output width");
-    NVFP4_REQUIRE(aligned16(x_dev) && aligned16(codes_dev) && aligned16(scales_dev), NVFP4_ERR_ALIGNMENT,
-                  "moe_nvfp4_gemv: pointers must be 16-byte aligned");
+    NVFP4_REQUIRE(aligned16(x_dev) && aligned16(codes_dev) && aligned16(scales_dev) &&
+                  reinterpret_cast<uintptr_t>(out_dev) % (epilogue == MOE_EPI_SWIGLU_BF16 ? 2 : 4) == 0,
+                  NVFP4_ERR_ALIGNMENT,
+                  "moe_nvfp4_gemv: x, codes and scales must be 16-byte aligned, out aligned to its elements");
     const size_t need = moe_nvfp4_gemv_workspace_size(T, N, E, k_r, epilogue);
     NVFP4_REQUIRE(need == 0 || (workspace && workspace_bytes >= need && aligned16(workspace)), NVFP4_ERR_WORKSPACE,
                   "moe_nvfp4_gemv: workspace of %zu bytes required", need);

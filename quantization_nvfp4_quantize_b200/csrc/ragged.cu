@@ -727,8 +727,8 @@ extern "C" nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t 
     NVFP4_REQUIRE(lda >= in && lda % 8 == 0, NVFP4_ERR_ALIGNMENT,
                   "moe_ragged_gemm: lda must be >= the input width and a multiple of 8");
     NVFP4_REQUIRE(ld_out >= outw, NVFP4_ERR_ALIGNMENT, "moe_ragged_gemm: ld_out must be >= the output width");
-    NVFP4_REQUIRE(aligned16(a_dev) && aligned16(w_dev), NVFP4_ERR_ALIGNMENT,
-                  "moe_ragged_gemm: a and w must be 16-byte aligned");
+    NVFP4_REQUIRE(aligned16(a_dev) && aligned16(w_dev) && reinterpret_cast<uintptr_t>(out_dev) % (out_f32 ? 4 : 2) == 0,
+                  NVFP4_ERR_ALIGNMENT, "moe_ragged_gemm: a and w must be 16-byte aligned, out aligned to its elements");
     CUtensorMap tm_m, tm_n;
     const CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B;
     const CUtensorMapDataType bf = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -782,6 +782,8 @@ extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t
     NVFP4_REQUIRE(E >= 1 && E <= MAX_E, NVFP4_ERR_UNSUPPORTED_SHAPE, "moe_ragged_wgrad: 1 <= E <= 256");
     if (N == 0 || K == 0) return NVFP4_OK;
     NVFP4_REQUIRE(out_dev, NVFP4_ERR_INVALID_ARG, "moe_ragged_wgrad: null pointer");
+    NVFP4_REQUIRE(reinterpret_cast<uintptr_t>(out_dev) % (out_f32 ? 4 : 2) == 0, NVFP4_ERR_ALIGNMENT,
+                  "moe_ragged_wgrad: out must be aligned to its elements");
     if (M == 0) {
         if (accumulate) return NVFP4_OK;
         if (cudaMemsetAsync(out_dev, 0, (size_t)E * N * K * (out_f32 ? 4 : 2), st) != cudaSuccess)

@@ -92,6 +92,20 @@ def test_training_step(cuda, T, E, H, I, kr):
     assert torch.equal(g2.dw13, 2 * g.dw13) and torch.equal(g2.dw2, 2 * g.dw2)
 
 
+def test_backward_again_and_after_other_calls(cuda):
+    """backward reads only what forward_train kept: a second one, and one after
+    an inference forward of the same layer, give the same bits."""
+    T, E, H, I, kr = 96, 4, 256, 128, 2
+    lay, _, _ = layer(MoELayerW4A16, T, E, H, I, kr)
+    x, logits, dy = rnd(20, T, H), rnd(21, T, E, dtype=torch.float32), rnd(22, T, H)
+    lay.forward_train(x, logits)
+    a = lay.backward(dy)
+    lay.forward(rnd(23, T, H), rnd(24, T, E, dtype=torch.float32))
+    b = lay.backward(dy)
+    for n in ("dx", "dlogits", "dw13", "dw2"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+
+
 def test_training_step_captured(cuda):
     T, E, H, I, kr = 64, 8, 128, 64, 2
     lay, w13, w2 = layer(MoELayerW4A16, T, E, H, I, kr)
@@ -157,6 +171,36 @@ def test_decode_step(cuda, t, E, H, I, kr):
     h = bf(a * torch.sigmoid(a) * b)
     want = (torch.einsum("tjhi,tji->tjh", v2[idx.indices], h) * g[..., None]).sum(1)
     assert rel_fro(y.double().cpu().numpy(), want.cpu().numpy()) <= TOL
+
+
+def test_decode_captured_and_two_batches_in_flight(cuda):
+    """Graph replays with new inputs, and two batches on two streams."""
+    E, H, I, kr = 16, 512, 256, 4
+    lay, _, _ = layer(MoELayerW4A4, 64, E, H, I, kr, 0)
+    x, logits = rnd(30, 5, H), rnd(31, 5, E, dtype=torch.float32)
+    lay.decode(x, logits)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = lay.decode(x, logits)
+    x.copy_(rnd(32, 5, H))
+    logits.copy_(rnd(33, 5, E, dtype=torch.float32))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y, lay.decode(x, logits))
+    xs = [rnd(34 + i, 40, H) for i in range(2)]
+    ls = [rnd(36 + i, 40, E, dtype=torch.float32) for i in range(2)]
+    want = [lay.decode(a, b) for a, b in zip(xs, ls)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(lay.decode(xs[i], ls[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert torch.equal(g, want[i])
 
 
 def test_dense_decode(cuda):

@@ -25,6 +25,7 @@ def test_ragged_gemm():
     #       a     lda  M    w     N    K   E  off  tr  out   ld  f32 stat  stream
     good = [FAKE, 64, 100, FAKE, 128, 64, 4, FAKE, 0, FAKE, 128, 0, None, None]
     calls("moe_ragged_gemm", good, [
+        (9, ctypes.c_void_p(0x10001), ALIGN),
         (0, None, INVALID), (3, None, INVALID), (7, None, INVALID), (9, None, INVALID), (2, -1, INVALID),
         (4, -1, INVALID), (6, 0, SHAPE), (6, 257, SHAPE), (2, 1 << 31, SHAPE), (4, 1 << 24, SHAPE), (5, 60, ALIGN),
         (1, 56, ALIGN), (1, 68, ALIGN), (10, 127, ALIGN), (0, ODD, ALIGN), (3, ODD, ALIGN), (5, 0, SHAPE)])
@@ -43,6 +44,7 @@ def test_ragged_wgrad():
     #       g     ldg  M    a     lda asc   lds rows  T   N    K   E  off   out   f32 acc ws  n  stat  stream
     good = [FAKE, 256, 5000, FAKE, 256, None, 0, None, 0, 256, 256, 128, FAKE, FAKE, 1, 0, None, 0, None, None]
     calls("moe_ragged_wgrad", good, [
+        (13, ctypes.c_void_p(0x10002), ALIGN),
         (0, None, INVALID), (3, None, INVALID), (12, None, INVALID), (13, None, INVALID), (2, -1, INVALID),
         (8, -1, INVALID), (11, 0, SHAPE), (11, 257, SHAPE), (2, 1 << 31, SHAPE), (1, 255, ALIGN), (1, 248, ALIGN),
         (4, 248, ALIGN), (4, 260, ALIGN), (0, ODD, ALIGN), (3, ODD, ALIGN), (7, FAKE, INVALID)])
@@ -111,6 +113,7 @@ def test_gemv():
     #       x     T  ldx   codes sc    s_t   N    K    E  idx  kr epi gate  out   ld  ws    n  stream
     good = [FAKE, 2, 128, FAKE, FAKE, FAKE, 256, 128, 8, FAKE, 2, 0, None, FAKE, 256, None, 0, None]
     calls("moe_nvfp4_gemv", good, [
+        (13, ctypes.c_void_p(0x10002), ALIGN),
         (0, None, INVALID), (3, None, INVALID), (4, None, INVALID), (5, None, INVALID), (13, None, INVALID),
         (9, None, INVALID), (11, 2, INVALID), (11, 4, INVALID), (1, -1, INVALID), (7, 96, SHAPE), (7, 0, SHAPE),
         (6, 0, SHAPE), (8, 0, SHAPE), (10, 0, SHAPE), (10, 33, SHAPE), (2, 120, ALIGN), (2, 132, ALIGN),
