@@ -128,3 +128,23 @@ def check(status: int) -> None:
     if status != 0:
         msg = load().nvfp4_last_error_string()
         raise Nvfp4Error(status, msg.decode() if msg else "")
+
+
+_bound = None
+
+
+def binding():
+    """The compiled half of the binding, with the library's entry points bound
+    (raises if either is not built)."""
+    global _bound
+    if _bound is None:
+        lib = load()
+        try:
+            import torch  # noqa: F401  (its libraries are the module's)
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"_binding.so is not built for this torch ({e}); run __graft_entry__.build() or "
+                               "python quantization_nvfp4_quantize_b200/build.py") from e
+        _binding.bind(check, {name: ctypes.cast(getattr(lib, name), c_void_p).value for name in SIGNATURES})
+        _bound = _binding
+    return _bound

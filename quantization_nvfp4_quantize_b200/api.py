@@ -2,13 +2,14 @@
 
 Each function only allocates output buffers with torch (device memory is
 PyTorch's), marshals pointers and sizes, and calls the library on the current
-CUDA stream; every step of the computation runs in the library's kernels.
+CUDA stream; every step of the computation runs in the library's kernels.  The
+marshalling is ctypes, and compiled (csrc/binding.cpp) where short calls would
+spend their time in it.
 There is no CPU or PyTorch fallback.
 """
 from __future__ import annotations
 
 import dataclasses
-import functools
 
 import torch
 
@@ -332,78 +333,16 @@ class Act8:
     codes: torch.Tensor          # uint8 [M, K], row stride a multiple of 16
     scales: torch.Tensor         # uint8 [M, 4 * ceil(K / 128)]
 
-    def get_device(self) -> int:
-        return self.codes.get_device()
+    @staticmethod
+    def empty(M: int, K: int, device) -> "Act8":
+        return Act8(torch.empty(M, -(-K // 16) * 16, dtype=U8, device=device)[:, :K],
+                    torch.empty(M, -(-K // 128) * 4, dtype=U8, device=device))
 
 
 # The experts' training and decode operators.  Their short calls last a few
-# microseconds on the device, so the checks below are written to cost little.
+# microseconds, so the marshalling (checks, outputs, workspaces, stream) is
+# compiled: csrc/binding.cpp.
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_empty = torch.empty
-
-
-def _on_device(fn):
-    """Refuse host tensors; run with the first argument's device current (the
-    library launches on the current device)."""
-    @functools.wraps(fn)
-    def call(x, *args, **kwargs):
-        i = x.get_device()
-        if i < 0:
-            raise ValueError("the NVFP4 kernels run on CUDA tensors only (got a tensor on cpu); there is no CPU path")
-        if i != _current_device():
-            with torch.cuda.device(i):
-                return fn(x, *args, **kwargs)
-        return fn(x, *args, **kwargs)
-    return call
-
-
-def _matrix(t, name, dtype, rows, cols, index):
-    """Row stride of a [rows, cols] tensor (rows None: any) of `dtype` on
-    device `index` with contiguous columns; a single row has none: its width
-    rounded up to 16."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype is not dtype or len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
-        raise ValueError(f"{name}: need {dtype} [{'rows' if rows is None else rows}, {cols}], got {t.dtype} {tuple(shape)}")
-    if stride[1] != 1 and cols > 1:
-        raise ValueError(f"{name}: columns must be contiguous")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
-    return stride[0] if shape[0] > 1 else -(-cols // 16) * 16
-
-
-def _vector(t, name, dtype, n, index):
-    """Address of n contiguous elements."""
-    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name}: need contiguous {dtype} with {n} elements, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != index:
-        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
-    return t.data_ptr()
-
-
-def _act8(a: Act8, name, rows, cols, index):
-    """(row stride of the codes, of the scales)."""
-    ldc = _matrix(a.codes, name + ".codes", U8, rows, cols, index)
-    s = a.scales
-    shape, stride = s.shape, s.stride()
-    if s.dtype is not U8 or len(shape) != 2 or shape[0] != a.codes.shape[0] or shape[1] < -(-cols // 128) * 4 \
-            or (stride[1] != 1 and shape[1] > 1):
-        raise ValueError(f"{name}.scales: need uint8 [{a.codes.shape[0]}, {-(-cols // 128) * 4}], got {s.dtype} "
-                         f"{tuple(shape)}")
-    if s.get_device() != index:
-        raise ValueError(f"{name}.scales: on {s.device}, expected cuda:{index}")
-    return ldc, stride[0] if shape[0] > 1 else -(-cols // 128) * 4
-
-
-def _act8_empty(M, K, device):
-    ld = -(-K // 16) * 16
-    codes = _empty(M, ld, dtype=U8, device=device)
-    return Act8(codes if ld == K else codes[:, :K], _empty(M, -(-K // 128) * 4, dtype=U8, device=device))
-
-
-@_on_device
 def ragged_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, transpose: bool = False,
                 out: torch.Tensor | None = None, out_dtype: torch.dtype = BF16, dev_status=None):
     """moe_ragged_gemm (see the header): row r of expert e (offsets[e] <= r <
@@ -411,27 +350,9 @@ def ragged_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, tran
     gradient).  a bf16 [M, K] (transpose: [M, N]), w bf16 [E, N, K].  Rows
     outside the segments are not written: pass `out` to keep what they hold
     (without it they are uninitialized)."""
-    lib = _lib.load()
-    i = a.get_device()
-    if w.dim() != 3 or w.dtype is not BF16 or not w.is_contiguous() or w.get_device() != i:
-        raise ValueError("ragged_gemm: w must be contiguous bf16 [E, N, K] on a's device")
-    E, N, K = w.shape
-    width = K if transpose else N
-    lda = _matrix(a, "ragged_gemm: a", BF16, None, N if transpose else K, i)
-    M = a.shape[0]
-    if out is None:
-        if out_dtype not in (BF16, F32):
-            raise ValueError("ragged_gemm: out_dtype must be bfloat16 or float32")
-        out = _empty(M, width, dtype=out_dtype, device=a.device)
-    f32 = out.dtype is F32
-    ldo = _matrix(out, "ragged_gemm: out", F32 if f32 else BF16, M, width, i)
-    check(lib.moe_ragged_gemm(a.data_ptr(), lda, M, w.data_ptr(), N, K, E,
-                              _vector(offsets, "ragged_gemm: offsets", I32, E + 1, i), transpose, out.data_ptr(), ldo,
-                              f32, _p(dev_status), _raw_stream(i)))
-    return out
+    return (_lib._bound or _lib.binding()).ragged_gemm(a, w, offsets, transpose, out, out_dtype, dev_status)
 
 
-@_on_device
 def ragged_wgrad(g: torch.Tensor, a, offsets: torch.Tensor, *, a_rows: torch.Tensor | None = None,
                  out: torch.Tensor | None = None, out_dtype: torch.dtype = F32, accumulate: bool = False,
                  dev_status=None):
@@ -439,168 +360,59 @@ def ragged_wgrad(g: torch.Tensor, a, offsets: torch.Tensor, *, a_rows: torch.Ten
     g[r]^T a[r].  g bf16 [M, N]; a bf16 [M, K], or an Act8 [T, K] whose row
     a_rows[r] (int32 [M]; without it row r) belongs to row r.  accumulate adds
     to `out`."""
-    lib = _lib.load()
-    i = g.get_device()
-    if g.dim() != 2:
-        raise ValueError("ragged_wgrad: g must be bf16 [M, N]")
-    M, N = g.shape
-    ldg = _matrix(g, "ragged_wgrad: g", BF16, M, N, i)
-    E = offsets.numel() - 1
-    off = _vector(offsets, "ragged_wgrad: offsets", I32, E + 1, i)
-    kept = isinstance(a, Act8)
-    if kept:
-        T, K = a.codes.shape
-        lda, lds = _act8(a, "ragged_wgrad: a", T if a_rows is not None else M, K, i)
-        data, scales = a.codes.data_ptr(), a.scales.data_ptr()
-    else:
-        T, K = M, a.shape[-1]
-        lda, lds = _matrix(a, "ragged_wgrad: a", BF16, M, K, i), 0
-        data, scales = a.data_ptr(), None
-    rows = None if a_rows is None else _vector(a_rows, "ragged_wgrad: a_rows", I32, M, i)
-    if out is None:
-        if accumulate:
-            raise ValueError("ragged_wgrad: accumulate needs out")
-        if out_dtype not in (BF16, F32):
-            raise ValueError("ragged_wgrad: out_dtype must be bfloat16 or float32")
-        out = _empty(E, N, K, dtype=out_dtype, device=g.device)
-    elif out.dtype not in (BF16, F32) or out.shape != (E, N, K) or not out.is_contiguous() or out.get_device() != i:
-        raise ValueError(f"ragged_wgrad: out must be contiguous bf16 or f32 [{E}, {N}, {K}] on g's device")
-    need = lib.moe_ragged_wgrad_workspace_size(M, N, K, E, kept)
-    ws = _empty(need, dtype=U8, device=g.device) if need else None
-    check(lib.moe_ragged_wgrad(g.data_ptr(), ldg, M, data, lda, scales, lds, rows, T, N, K, E, off, out.data_ptr(),
-                               out.dtype is F32, accumulate, _p(ws), need, _p(dev_status), _raw_stream(i)))
-    return out
+    b = _lib._bound or _lib.binding()
+    if isinstance(a, Act8):
+        return b.ragged_wgrad(g, a.codes, a.scales, offsets, a_rows, out, out_dtype, accumulate, dev_status)
+    return b.ragged_wgrad(g, a, None, offsets, a_rows, out, out_dtype, accumulate, dev_status)
 
 
-@_on_device
 def act8_quantize(x: torch.Tensor, *, out: Act8 | None = None) -> Act8:
     """act8_quantize (see the header): bf16 [M, K] kept in 8 bits."""
-    lib = _lib.load()
-    i = x.get_device()
-    if x.dim() != 2:
-        raise ValueError("act8_quantize: x must be bf16 [M, K]")
-    M, K = x.shape
-    ldx = _matrix(x, "act8_quantize: x", BF16, M, K, i)
-    if out is None:
-        out = _act8_empty(M, K, x.device)
-    ldc, lds = _act8(out, "act8_quantize: out", M, K, i)
-    check(lib.act8_quantize(x.data_ptr(), M, K, ldx, out.codes.data_ptr(), ldc, out.scales.data_ptr(), lds,
-                            _raw_stream(i)))
-    return out
+    b = _lib._bound or _lib.binding()
+    if out is not None:
+        b.act8_quantize(x, out.codes, out.scales)
+        return out
+    return Act8(*b.act8_quantize(x, None, None))
 
 
-@_on_device
 def act8_dequantize(a: Act8, *, out: torch.Tensor | None = None) -> torch.Tensor:
     """act8_dequantize: the kept values as bf16 [M, K] (exact)."""
-    lib = _lib.load()
-    i = a.get_device()
-    M, K = a.codes.shape
-    ldc, lds = _act8(a, "act8_dequantize: a", M, K, i)
-    if out is None:
-        out = _empty(M, -(-K // 8) * 8, dtype=BF16, device=a.codes.device)[:, :K]
-    ldx = _matrix(out, "act8_dequantize: out", BF16, M, K, i)
-    check(lib.act8_dequantize(a.codes.data_ptr(), ldc, a.scales.data_ptr(), lds, M, K, out.data_ptr(), ldx,
-                              _raw_stream(i)))
-    return out
+    return (_lib._bound or _lib.binding()).act8_dequantize(a.codes, a.scales, out)
 
 
-@_on_device
 def swiglu_act8(y: torch.Tensor, *, h: torch.Tensor | None = None, out: Act8 | None = None):
     """moe_swiglu_act8 (see the header): (h = silu(gate) * up, y kept in 8
     bits) of y = [gate | up], bf16 [M, 2I]."""
-    lib = _lib.load()
-    i = y.get_device()
-    if y.dim() != 2 or y.shape[1] % 2:
-        raise ValueError("swiglu_act8: y must be bf16 [M, 2I]")
-    M, K = y.shape
-    I = K // 2
-    ldy = _matrix(y, "swiglu_act8: y", BF16, M, K, i)
-    if h is None:
-        h = _empty(M, I, dtype=BF16, device=y.device)
-    if out is None:
-        out = _act8_empty(M, K, y.device)
-    ldh = _matrix(h, "swiglu_act8: h", BF16, M, I, i)
-    ldc, lds = _act8(out, "swiglu_act8: out", M, K, i)
-    check(lib.moe_swiglu_act8(y.data_ptr(), M, I, ldy, h.data_ptr(), ldh, out.codes.data_ptr(), ldc,
-                              out.scales.data_ptr(), lds, _raw_stream(i)))
-    return h, out
+    b = _lib._bound or _lib.binding()
+    if out is not None:
+        return b.swiglu_act8(y, h, out.codes, out.scales)[0], out
+    h, codes, scales = b.swiglu_act8(y, h, None, None)
+    return h, Act8(codes, scales)
 
 
-@_on_device
 def swiglu_act8_backward(y: Act8, dh: torch.Tensor, *, row_gate: torch.Tensor | None = None,
                          dy: torch.Tensor | None = None, gh: torch.Tensor | None = None,
                          dgate: torch.Tensor | None = None):
     """moe_swiglu_act8_backward (see the header): (dy [M, 2I], gate-weighted h
     [M, I], dgate f32 [M]) from the kept y and the gradient dh bf16 [M, I] of
     the unweighted h."""
-    lib = _lib.load()
-    i = y.get_device()
-    if dh.dim() != 2:
-        raise ValueError("swiglu_act8_backward: dh must be bf16 [M, I]")
-    M, I = dh.shape
-    lddh = _matrix(dh, "swiglu_act8_backward: dh", BF16, M, I, i)
-    ldc, lds = _act8(y, "swiglu_act8_backward: y", M, 2 * I, i)
-    gate = None if row_gate is None else _vector(row_gate, "swiglu_act8_backward: row_gate", F32, M, i)
-    dev = dh.device
-    if dy is None:
-        dy = _empty(M, 2 * I, dtype=BF16, device=dev)
-    if gh is None:
-        gh = _empty(M, I, dtype=BF16, device=dev)
-    if dgate is None:
-        dgate = _empty(M, dtype=F32, device=dev)
-    lddy = _matrix(dy, "swiglu_act8_backward: dy", BF16, M, 2 * I, i)
-    ldgh = _matrix(gh, "swiglu_act8_backward: gh", BF16, M, I, i)
-    check(lib.moe_swiglu_act8_backward(y.codes.data_ptr(), ldc, y.scales.data_ptr(), lds, dh.data_ptr(), lddh, gate, M,
-                                       I, dy.data_ptr(), lddy, gh.data_ptr(), ldgh,
-                                       _vector(dgate, "swiglu_act8_backward: dgate", F32, M, i), _raw_stream(i)))
-    return dy, gh, dgate
+    return (_lib._bound or _lib.binding()).swiglu_act8_backward(y.codes, y.scales, dh, row_gate, dy, gh, dgate)
 
 
-@_on_device
 def combine_rows(rows: torch.Tensor, dst_row: torch.Tensor, *, gate: torch.Tensor | None = None,
                  out: torch.Tensor | None = None) -> torch.Tensor:
     """moe_combine_rows: out[t] = sum_j gate[t, j] rows[dst_row[t, j]] (f32,
     slot order); rows bf16 [M, H], dst_row int32 [T, k_r]."""
-    lib = _lib.load()
-    i = rows.get_device()
-    if rows.dim() != 2 or dst_row.dim() != 2:
-        raise ValueError("combine_rows: rows must be bf16 [M, H], dst_row int32 [T, k_r]")
-    M, H = rows.shape
-    T, kr = dst_row.shape
-    ldr = _matrix(rows, "combine_rows: rows", BF16, M, H, i)
-    if out is None:
-        out = _empty(T, H, dtype=F32, device=rows.device)
-    ldo = _matrix(out, "combine_rows: out", F32, T, H, i)
-    check(lib.moe_combine_rows(rows.data_ptr(), M, H, ldr, _vector(dst_row, "combine_rows: dst_row", I32, T * kr, i),
-                               None if gate is None else _vector(gate, "combine_rows: gate", F32, T * kr, i), T, kr,
-                               out.data_ptr(), ldo, _raw_stream(i)))
-    return out
+    return (_lib._bound or _lib.binding()).combine_rows(rows, dst_row, gate, out)
 
 
-@_on_device
 def route_backward(topk_idx: torch.Tensor, topk_gate: torch.Tensor, dst_row: torch.Tensor, dgate_row: torch.Tensor,
                    E: int, *, out: torch.Tensor | None = None) -> torch.Tensor:
     """moe_route_backward: the router logits' gradient f32 [T, E] from the
     routed rows' gate gradients dgate_row f32 [M]."""
-    lib = _lib.load()
-    i = topk_idx.get_device()
-    if topk_idx.dim() != 2 or dgate_row.dim() != 1:
-        raise ValueError("route_backward: topk_idx must be int32 [T, k_r], dgate_row float32 [M]")
-    T, kr = topk_idx.shape
-    M = dgate_row.numel()
-    if out is None:
-        out = _empty(T, E, dtype=F32, device=topk_idx.device)
-    elif out.dtype is not F32 or out.shape != (T, E) or not out.is_contiguous() or out.get_device() != i:
-        raise ValueError(f"route_backward: out must be contiguous float32 [{T}, {E}]")
-    check(lib.moe_route_backward(_vector(topk_idx, "route_backward: topk_idx", I32, T * kr, i),
-                                 _vector(topk_gate, "route_backward: topk_gate", F32, T * kr, i),
-                                 _vector(dst_row, "route_backward: dst_row", I32, T * kr, i),
-                                 _vector(dgate_row, "route_backward: dgate_row", F32, M, i), M, T, E, kr,
-                                 out.data_ptr(), _raw_stream(i)))
-    return out
+    return (_lib._bound or _lib.binding()).route_backward(topk_idx, topk_gate, dst_row, dgate_row, E, out)
 
 
-@_on_device
 def nvfp4_gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s_t: torch.Tensor, N: int, K: int, *,
                expert_idx: torch.Tensor | None = None, epilogue: int = EPI_STORE_F32,
                gate: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
@@ -609,42 +421,7 @@ def nvfp4_gemv(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, s_t: 
     them).  expert_idx int32 [T, k_r] names each token's experts; None: one
     dense weight.  x has one row per token (EPI_COMBINE_F32: per token and
     slot, with the router weights `gate` f32 [T, k_r])."""
-    lib = _lib.load()
-    i = x.get_device()
-    ldx = _matrix(x, "nvfp4_gemv: x", BF16, None, K, i)
-    rows = x.shape[0]
-    E = s_t.numel()
-    if codes.dtype is not U8 or not codes.is_contiguous() or codes.numel() * 2 != E * N * K or codes.get_device() != i:
-        raise ValueError(f"nvfp4_gemv: codes must be contiguous uint8 [{E}, {N}, {K // 2}] on x's device")
-    if scales.dtype is not U8 or not scales.is_contiguous() or scales.numel() < E * scale_bytes(N, K) \
-            or scales.get_device() != i:
-        raise ValueError(f"nvfp4_gemv: scales must be contiguous uint8 with {E * scale_bytes(N, K)} bytes on x's device")
-    combine = epilogue == EPI_COMBINE_F32
-    if expert_idx is None:
-        T, kr, idx = rows, 1, None
-    else:
-        if expert_idx.dim() != 2:
-            raise ValueError("nvfp4_gemv: expert_idx must be int32 [T, k_r]")
-        T, kr = expert_idx.shape
-        idx = _vector(expert_idx, "nvfp4_gemv: expert_idx", I32, T * kr, i)
-        if rows != (T * kr if combine else T):
-            raise ValueError(f"nvfp4_gemv: x has {rows} rows for {T} tokens with {kr} experts each")
-    if gate is not None:
-        if not combine:
-            raise ValueError("nvfp4_gemv: gate goes with EPI_COMBINE_F32")
-        gate = _vector(gate, "nvfp4_gemv: gate", F32, T * kr, i)
-    swiglu = epilogue == EPI_SWIGLU_BF16
-    dtype, width = (BF16, N // 2) if swiglu else (F32, N)
-    orows = T if combine else T * kr
-    if out is None:
-        out = _empty(orows, width, dtype=dtype, device=x.device)
-    ldo = _matrix(out, "nvfp4_gemv: out", dtype, orows, width, i)
-    need = lib.moe_nvfp4_gemv_workspace_size(T, N, E, kr, epilogue) if combine else 0
-    ws = _empty(need, dtype=U8, device=x.device) if need else None
-    check(lib.moe_nvfp4_gemv(x.data_ptr(), T, ldx, codes.data_ptr(), scales.data_ptr(),
-                             _vector(s_t, "nvfp4_gemv: s_t", F32, E, i), N, K, E, idx, kr, epilogue, gate,
-                             out.data_ptr(), ldo, _p(ws), need, _raw_stream(i)))
-    return out
+    return (_lib._bound or _lib.binding()).nvfp4_gemv(x, codes, scales, s_t, N, K, expert_idx, epilogue, gate, out)
 
 
 def debug_encode(v: torch.Tensor):

@@ -1,4 +1,6 @@
-"""Build the sm_100a shared library ``libnvfp4_quads.so`` in-tree with nvcc.
+"""Build the sm_100a shared library ``libnvfp4_quads.so`` in-tree with nvcc, and
+the compiled half of the Python binding (``_binding.so``, host code only) with
+g++ against the installed torch's headers.
 
 Every translation unit under ``csrc/`` is compiled for
 ``-gencode arch=compute_100a,code=sm_100a`` (no other architecture, no
@@ -19,6 +21,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libnvfp4_quads.so")
+BINDING = os.path.join(HERE, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
@@ -51,15 +54,37 @@ def _compile(src: str, verbose_ptxas: bool) -> str:
     return obj
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile csrc/binding.cpp into the extension module _binding.so."""
+    import sysconfig
+
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    root = os.path.dirname(torch.__file__)
+    if force or _stale(BINDING, [src, os.path.join(root, "version.py")] + _headers()):
+        tmp = BINDING + ".tmp%d" % os.getpid()
+        dirs = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+        subprocess.check_call(["g++", "-std=c++17", "-O2", "-fPIC", "-shared", "-fvisibility=hidden",
+                               *[f for d in dirs for f in ("-isystem", d)], src, "-o", tmp,
+                               "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu",
+                               "-lc10_cuda", "-lc10"])
+        os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
-    """Compile csrc/*.cu and link libnvfp4_quads.so; returns its path."""
+    """Compile csrc/*.cu and link libnvfp4_quads.so (returns its path), and
+    build the binding."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if force:
         for o in glob.glob(os.path.join(BUILD, "*.o")):
             os.remove(o)
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
+        binding = ex.submit(build_binding, force)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        binding.result()
     if _stale(LIB, objs):
         tmp = LIB + ".tmp%d" % os.getpid()
         subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs,

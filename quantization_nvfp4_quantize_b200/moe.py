@@ -264,8 +264,8 @@ class MoELayerW4A16:
         self.h_t = torch.empty(m, I, **bf)              # h, later its gradient
         self.gh = torch.empty(m, I, **bf)               # router-weighted h
         self.dgate = torch.empty(m, dtype=torch.float32, device=dev)
-        self.x8 = api._act8_empty(self.T, H, dev)       # kept between forward_train and backward
-        self.y8 = api._act8_empty(m, 2 * I, dev)
+        self.x8 = api.Act8.empty(self.T, H, dev)       # kept between forward_train and backward
+        self.y8 = api.Act8.empty(m, 2 * I, dev)
 
     def forward_train(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """The layer with what backward needs kept in 8 bits: X (per token, not

@@ -140,45 +140,92 @@ def test_route_accepts_unpadded_segments():
     assert lib.moe_route(FAKE, 16, 8, 2, FAKE, FAKE, 2, FAKE, FAKE, FAKE, FAKE, 64, FAKE, 4096, None) == INVALID
 
 
+def good_calls():
+    """Well-formed operands on the host: refused for their device alone."""
+    bf, f32, i32, u8 = (lambda *n: torch.zeros(*n, dtype=torch.bfloat16)), torch.zeros, \
+        (lambda *n: torch.zeros(*n, dtype=torch.int32)), (lambda *n: torch.zeros(*n, dtype=torch.uint8))
+    a8 = lambda m, k: api.Act8(u8(m, k), u8(m, -(-k // 128) * 4))
+    return {
+        "ragged_gemm": lambda **k: api.ragged_gemm(**{**dict(a=bf(4, 64), w=bf(2, 16, 64), offsets=i32(3)), **k}),
+        "ragged_wgrad": lambda **k: api.ragged_wgrad(**{**dict(g=bf(4, 16), a=bf(4, 64), offsets=i32(3)), **k}),
+        "ragged_wgrad kept": lambda **k: api.ragged_wgrad(**{**dict(g=bf(4, 16), a=a8(4, 64), offsets=i32(3)), **k}),
+        "act8_quantize": lambda **k: api.act8_quantize(**{**dict(x=bf(4, 64)), **k}),
+        "act8_dequantize": lambda **k: api.act8_dequantize(**{**dict(a=a8(4, 64)), **k}),
+        "swiglu_act8": lambda **k: api.swiglu_act8(**{**dict(y=bf(4, 64)), **k}),
+        "swiglu_act8_backward": lambda **k: api.swiglu_act8_backward(**{**dict(y=a8(4, 64), dh=bf(4, 32)), **k}),
+        "combine_rows": lambda **k: api.combine_rows(**{**dict(rows=bf(4, 64), dst_row=i32(2, 2)), **k}),
+        "route_backward": lambda **k: api.route_backward(**{**dict(topk_idx=i32(2, 2), topk_gate=f32(2, 2),
+                                                                   dst_row=i32(2, 2), dgate_row=f32(4), E=8), **k}),
+        "nvfp4_gemv": lambda **k: api.nvfp4_gemv(**{**dict(x=bf(2, 64), codes=u8(3, 32, 32), scales=u8(3, 512), s_t=f32(3),
+                                                           N=32, K=64, expert_idx=i32(2, 2)), **k}),
+    }
+
+
 def test_binding_refuses_host_tensors():
-    bf = torch.zeros(4, 64, dtype=torch.bfloat16)
-    u8 = torch.zeros(4, 64, dtype=torch.uint8)
-    off = torch.zeros(3, dtype=torch.int32)
-    a8 = api.Act8(u8, u8)
-    for call in (lambda: api.ragged_gemm(bf, bf.view(1, 4, 64), off), lambda: api.ragged_wgrad(bf, bf, off),
-                 lambda: api.act8_quantize(bf), lambda: api.act8_dequantize(a8), lambda: api.swiglu_act8(bf),
-                 lambda: api.swiglu_act8_backward(a8, bf), lambda: api.combine_rows(bf, off.view(1, 3)),
-                 lambda: api.route_backward(off.view(1, 3), off.view(1, 3).float(), off.view(1, 3), off.float(), 4),
-                 lambda: api.nvfp4_gemv(bf, u8, u8, off.float(), 4, 64)):
+    for name, call in good_calls().items():
         with pytest.raises(ValueError, match="CUDA tensors only"):
             call()
 
 
-def test_binding_checks_operands():
-    t = torch.zeros(4, 8)                                    # a host tensor: device index -1
-    assert api._matrix(t, "x", torch.float32, 4, 8, -1) == 8
-    assert api._matrix(t[:1, :5], "x", torch.float32, None, 5, -1) == 16      # one row: no stride of its own
-    with pytest.raises(ValueError, match="need torch.bfloat16"):
-        api._matrix(t, "x", torch.bfloat16, 4, 8, -1)
-    with pytest.raises(ValueError, match="need"):
-        api._matrix(t, "x", torch.float32, 4, 9, -1)
-    with pytest.raises(ValueError, match="need"):
-        api._matrix(t, "x", torch.float32, 3, 8, -1)
-    with pytest.raises(ValueError, match="need"):
-        api._matrix(t.view(2, 2, 8), "x", torch.float32, 2, 2, -1)
-    with pytest.raises(ValueError, match="contiguous"):
-        api._matrix(t.t(), "x", torch.float32, 8, 4, -1)
-    with pytest.raises(ValueError, match="expected cuda:0"):
-        api._matrix(t, "x", torch.float32, 4, 8, 0)
-    with pytest.raises(ValueError, match="elements"):
-        api._vector(t, "x", torch.float32, 31, -1)
-    with pytest.raises(ValueError, match="elements"):
-        api._vector(t.t(), "x", torch.float32, 32, -1)
-    with pytest.raises(ValueError, match="expected cuda:0"):
-        api._vector(t, "x", torch.float32, 32, 0)
-    u8 = torch.zeros(4, 160, dtype=torch.uint8)
-    assert api._act8(api.Act8(u8, u8[:, :8]), "x", 4, 160, -1) == (160, 160)
-    with pytest.raises(ValueError, match="scales"):
-        api._act8(api.Act8(u8, u8[:, :4]), "x", 4, 160, -1)
-    with pytest.raises(ValueError, match="scales"):
-        api._act8(api.Act8(u8, u8[:3, :8]), "x", 4, 160, -1)
+def test_binding_refuses_operands():
+    bf, u8, i32 = (lambda *n: torch.zeros(*n, dtype=torch.bfloat16)), (lambda *n: torch.zeros(*n, dtype=torch.uint8)), \
+        (lambda *n: torch.zeros(*n, dtype=torch.int32))
+    a8 = api.Act8
+    meta = torch.zeros(4, 64, dtype=torch.bfloat16, device="meta")
+    bad = [
+        ("ragged_gemm", dict(a=torch.zeros(4, 64)), "a: need BFloat16"),
+        ("ragged_gemm", dict(a=bf(4, 56)), "a: need"),
+        ("ragged_gemm", dict(a=bf(64, 4).t()), "columns must be contiguous"),
+        ("ragged_gemm", dict(w=bf(16, 64)), "w must be"),
+        ("ragged_gemm", dict(w=bf(2, 64, 16).transpose(1, 2)), "w must be"),
+        ("ragged_gemm", dict(offsets=i32(4)), "3 elements"),
+        ("ragged_gemm", dict(offsets=torch.zeros(3, dtype=torch.int64)), "offsets: need"),
+        ("ragged_gemm", dict(out=bf(4, 17)), "out: need"),
+        ("ragged_gemm", dict(out_dtype=torch.float16), "out_dtype"),
+        ("ragged_gemm", dict(transpose=True), "a: need"),
+        ("ragged_gemm", dict(a=meta), "expected meta"),
+        ("ragged_gemm", dict(a=None), "need a tensor"),
+        ("ragged_wgrad", dict(a=bf(5, 64)), "a: need"),
+        ("ragged_wgrad", dict(g=bf(4)), "must be"),
+        ("ragged_wgrad", dict(out=torch.zeros(2, 64, 16)), "out must be"),
+        ("ragged_wgrad", dict(accumulate=True), "accumulate needs out"),
+        ("ragged_wgrad kept", dict(a=a8(u8(5, 64), u8(5, 4))), "a.codes: need"),
+        ("ragged_wgrad kept", dict(a=a8(u8(4, 64), u8(4, 3))), "a.scales: need"),
+        ("ragged_wgrad kept", dict(a=a8(u8(4, 64), u8(3, 4))), "a.scales: need"),
+        ("ragged_wgrad kept", dict(a_rows=i32(5)), "a_rows: need"),
+        ("act8_quantize", dict(x=bf(4)), "must be"),
+        ("act8_quantize", dict(x=torch.zeros(4, 64)), "x: need"),
+        ("act8_quantize", dict(out=a8(u8(4, 63), u8(4, 4))), "out.codes: need"),
+        ("act8_dequantize", dict(out=bf(4, 63)), "out: need"),
+        ("swiglu_act8", dict(y=bf(4, 63)), "must be"),
+        ("swiglu_act8", dict(h=bf(4, 33), out=a8(u8(4, 64), u8(4, 4))), "h: need"),
+        ("swiglu_act8_backward", dict(dh=bf(4, 31)), "y.codes: need"),
+        ("swiglu_act8_backward", dict(row_gate=torch.zeros(5)), "row_gate: need"),
+        ("combine_rows", dict(dst_row=i32(4)), "must be"),
+        ("combine_rows", dict(gate=torch.zeros(3)), "gate: need"),
+        ("route_backward", dict(dst_row=i32(3, 2)), "dst_row: need"),
+        ("route_backward", dict(E=0), "1 <= E"),
+        ("route_backward", dict(out=torch.zeros(2, 7)), "out must be"),
+        ("nvfp4_gemv", dict(x=bf(3, 64)), "rows for 2 tokens"),
+        ("nvfp4_gemv", dict(codes=u8(3, 32, 31)), "codes must be"),
+        ("nvfp4_gemv", dict(scales=u8(3, 511)), "scales must be"),
+        ("nvfp4_gemv", dict(gate=torch.zeros(2, 2)), "EPI_COMBINE"),
+        ("nvfp4_gemv", dict(expert_idx=i32(4)), "expert_idx must be"),
+        ("nvfp4_gemv", dict(N=0), "must be positive"),
+    ]
+    calls = good_calls()
+    for name, change, match in bad:
+        with pytest.raises(ValueError, match=match):
+            calls[name](**change)
+    with pytest.raises(TypeError):
+        _lib.binding().combine_rows(None)
+
+
+def test_missing_binding_fails_loudly(monkeypatch):
+    import sys
+    monkeypatch.setattr(_lib, "_bound", None)
+    monkeypatch.setitem(sys.modules, "quantization_nvfp4_quantize_b200._binding", None)
+    import quantization_nvfp4_quantize_b200 as pkg
+    monkeypatch.delattr(pkg, "_binding", raising=False)
+    with pytest.raises(RuntimeError, match="not built"):
+        _lib.binding()
