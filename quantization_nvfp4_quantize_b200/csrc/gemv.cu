@@ -50,12 +50,13 @@ struct Params {
     const uint8_t *codes;
     const uint8_t *scales;
     const float *s_t;
-    int64_t N, K;
+    int32_t N, K;
     int E;
+    int64_t code_stride, scale_stride;   // bytes of one expert's codes and scales
     const int32_t *idx;                  // experts of the pairs, or null (one dense weight)
     int pairs;                           // (token, slot) pairs (dense: tokens)
     int k_r;
-    int x_div;                           // row of x = pair / x_div
+    uint32_t x_mul;                      // row of x = pair * x_mul >> 16 (pair / k_r, or pair)
     const float *gate;
     void *out;
     int64_t ld_out;
@@ -95,47 +96,54 @@ __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, u
 }
 
 // Weight row of tile-local row rr (0..15): 4 rows of each 32-row quarter.
-__device__ __forceinline__ int64_t tile_row(int tile, int rr)
+__device__ __forceinline__ int tile_row(int tile, int rr)
 {
     const int g = rr & 7;
-    return (int64_t)(tile >> 3) * 128 + 32 * (g & 3) + 4 * (tile & 7) + (g >> 2) + 2 * (rr >> 3);
+    return (tile >> 3) * 128 + 32 * (g & 3) + 4 * (tile & 7) + (g >> 2) + 2 * (rr >> 3);
 }
 
-// A lane's pointers at column 32 t into one 16-row set: codes and scale words
-// of row g; row g + 8 (two weight rows further) lies c2 / s2 bytes on.  A row
-// past the end reads an existing one; its sums are not stored.
+// A lane's pointers into one 16-row set: codes and scale words of row g, column
+// 0; row g + 8 (two weight rows further) lies c2 / s2 bytes on.  A row past
+// the end reads an existing one; its sums are not stored.
 struct Set {
     const uint8_t *c;
     const uint8_t *s;
     int32_t c2, s2;
 };
 
-__device__ __forceinline__ Set set_of(const Params &p, int e, int tile, int64_t row_base, int64_t rows)
+__device__ __forceinline__ uint64_t scale_at(uint32_t n, uint32_t K)
 {
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-    const int64_t r = tile_row(tile, g);
-    const int64_t n = row_base + min(r, rows - 1);
+    return (uint64_t)(n >> 7) * (K * 8u) + (n & 31u) * 16u + ((n >> 5) & 3u) * 4u;
+}
+
+__device__ __forceinline__ Set set_of(const Params &p, const uint8_t *codes, const uint8_t *scales, int tile, int row_base,
+                                      int rows)
+{
+    const int r = tile_row(tile, (threadIdx.x & 31) >> 2);
+    const uint32_t n = (uint32_t)(row_base + min(r, rows - 1));
     Set l;
-    l.c = p.codes + ((int64_t)e * p.N + n) * (p.K / 2) + 16 * t;
-    l.s = p.scales + (int64_t)e * (((p.N + 127) / 128) * 128 * (p.K / 16)) + sf_offset(n, 0, p.K) + (t >> 1) * 512;
+    l.c = codes + (uint64_t)n * (uint32_t)(p.K >> 1);
+    l.s = scales + scale_at(n, (uint32_t)p.K);
     const bool second = r + 2 < rows;
-    l.c2 = second ? (int32_t)p.K : 0;
+    l.c2 = second ? p.K : 0;
     // rows n and n + 2 share a 32-row quarter unless the set straddles one (SwiGLU's up rows)
-    l.s2 = second ? (int32_t)(sf_offset(n + 2, 0, p.K) - sf_offset(n, 0, p.K)) : 0;
+    l.s2 = second ? (int32_t)(scale_at(n + 2, (uint32_t)p.K) - scale_at(n, (uint32_t)p.K)) : 0;
     return l;
 }
 
-// 128 columns of one set: codes c, scale byte pairs s of its two rows, the
-// lane's 32 x as pairs (i, i + 4) in xp.
-__device__ __forceinline__ void compute_chunk(const uint4 (&c)[2], const uint32_t (&s)[2], const uint32_t (&xp)[16],
-                                              float (&acc)[4])
+// 128 columns of one set: codes c and scale words s of its two rows, the
+// lane's two scale bytes being byte0 and byte0 + 1 of its word; the lane's 32 x
+// as pairs (i, i + 4) in xp.
+__device__ __forceinline__ void compute_chunk(const uint4 (&c)[2], const uint32_t (&s)[2], uint32_t byte0,
+                                              const uint32_t (&xp)[16], float (&acc)[4])
 {
     const uint32_t ca[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
     const uint32_t cb[4] = {c[1].x, c[1].y, c[1].z, c[1].w};
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
-        const uint32_t sa = scale_operand((s[0] >> (8 * blk)) & 0xFFu);
-        const uint32_t sb = scale_operand((s[1] >> (8 * blk)) & 0xFFu);
+        const uint32_t pick = 0x4440u + byte0 + blk;
+        const uint32_t sa = scale_operand(__byte_perm(s[0], 0u, pick));
+        const uint32_t sb = scale_operand(__byte_perm(s[1], 0u, pick));
 #pragma unroll
         for (int q = 2 * blk; q < 2 * blk + 2; ++q) {
             uint32_t pa[4], pb[4];
@@ -168,30 +176,44 @@ __device__ __forceinline__ void copy4(void *dst, const void *src)
 
 // Chunks of 128 columns ch0, ch0 + stride, ... below `chunks`, of SETS row sets
 // against the same x; DEPTH - 1 chunks are in flight while one is computed.
-// x: the lane's token row at column 32 t, or null (zeros).
+// x: the lane's token row, or null (zeros).  K is a multiple of 64, so half of
+// the last chunk may be missing: its lanes read earlier columns again, against
+// zeros of x.
 template <int SETS>
 __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS], const __nv_bfloat16 *x, int ch0,
-                                          int stride, int chunks, int64_t K, float (&acc)[SETS][4])
+                                          int stride, int chunks, int K, float (&acc)[SETS][4])
 {
     const int lane = threadIdx.x & 31, t = lane & 3;
-    const int n = ch0 < chunks ? (chunks - ch0 + stride - 1) / stride : 0;
-    auto inside = [&](int i) { return (int64_t)(ch0 + i * stride) * 128 + 32 * t < K; };
-    auto issue = [&](int i) {
-        if (i < n) {
-            // K is a multiple of 64: half of the last chunk may be missing.  A
-            // missing part reads columns 0..63 again, against zeros of x.
-            const bool in = inside(i);
-            const int64_t at = in ? ch0 + i * stride : 0;
-            const int64_t back = in ? 0 : t >> 1;
-            Slot<SETS> &slot = ring[i % DEPTH];
+    if (ch0 >= chunks) return;
+    const int n = (chunks - 1 - ch0) / stride + 1;
+    const int step = stride * 128;
+    int col = ch0 * 128 + 32 * t;                                 // of the next chunk to copy
+    const int at = col < K ? col : col - 64;
+    const uint8_t *pc[SETS], *ps[SETS];
+#pragma unroll
+    for (int k = 0; k < SETS; ++k) {
+        pc[k] = l[k].c + (at >> 1);
+        ps[k] = l[k].s + (uint64_t)(at >> 6) * 512;
+    }
+    int issued = 0;
+    auto issue = [&]() {
+        if (issued < n) {
+            Slot<SETS> &slot = ring[issued % DEPTH];
 #pragma unroll
             for (int k = 0; k < SETS; ++k) {
-                const uint8_t *pc = l[k].c + at * 64 - back * 32;
-                const uint8_t *ps = l[k].s + at * 1024 - back * 512;
-                copy16(&slot.c[2 * k][lane], pc);
-                copy16(&slot.c[2 * k + 1][lane], pc + l[k].c2);
-                copy4(&slot.s[lane][2 * k], ps);
-                copy4(&slot.s[lane][2 * k + 1], ps + l[k].s2);
+                copy16(&slot.c[2 * k][lane], pc[k]);
+                copy16(&slot.c[2 * k + 1][lane], pc[k] + l[k].c2);
+                copy4(&slot.s[lane][2 * k], ps[k]);
+                copy4(&slot.s[lane][2 * k + 1], ps[k] + l[k].s2);
+            }
+            ++issued;
+            col += step;
+            if (col < K) {
+#pragma unroll
+                for (int k = 0; k < SETS; ++k) {
+                    pc[k] += step / 2;
+                    ps[k] += step * 8;
+                }
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -199,23 +221,25 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
     uint4 v[4];                          // zeros where the lane has no token
 #pragma unroll
     for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
-    auto load_x = [&](int i) {
-        if (x != nullptr && i < n) {
-            if (inside(i)) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(x + (int64_t)(ch0 + i * stride) * 128);
+    int xcol = ch0 * 128 + 32 * t;
+    auto load_x = [&]() {
+        if (x != nullptr) {
+            if (xcol < K) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(x + xcol);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = __ldg(src + k);
-            } else {                     // the missing half of the last chunk
+            } else {                     // past the end, or the missing half of the last chunk
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
             }
+            xcol += step;
         }
     };
 #pragma unroll
-    for (int i = 0; i < DEPTH - 1; ++i) issue(i);
-    load_x(0);
+    for (int i = 0; i < DEPTH - 1; ++i) issue();
+    load_x();
     for (int i = 0; i < n; ++i) {
-        issue(i + DEPTH - 1);
+        issue();
         uint32_t xp[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -224,14 +248,14 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
             xp[4 * q + 2] = __byte_perm(v[q].y, v[q].w, 0x5410);
             xp[4 * q + 3] = __byte_perm(v[q].y, v[q].w, 0x7632);
         }
-        load_x(i + 1);
+        load_x();
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
         const Slot<SETS> &slot = ring[i % DEPTH];
 #pragma unroll
         for (int k = 0; k < SETS; ++k) {
             const uint4 c[2] = {slot.c[2 * k][lane], slot.c[2 * k + 1][lane]};
-            const uint32_t s[2] = {slot.s[lane][2 * k] >> (16 * (t & 1)), slot.s[lane][2 * k + 1] >> (16 * (t & 1))};
-            compute_chunk(c, s, xp, acc[k]);
+            const uint32_t s[2] = {slot.s[lane][2 * k], slot.s[lane][2 * k + 1]};
+            compute_chunk(c, s, 2 * (t & 1), xp, acc[k]);
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");          // nothing in flight when the ring is reused
@@ -255,12 +279,12 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_nvfp4_gemv(const Params p, 
     __shared__ int list[MAX_PAIRS];
     __shared__ int count;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int chunks = (int)((p.K + 127) / 128);
+    const int chunks = (p.K + 127) / 128;
     const int b = (int)blockIdx.x;
     const int per_block = WARPS / splits;                        // row pairs
     const int rp = (int)blockIdx.y * per_block + warp / splits;  // this warp's
     const int split = warp % splits;
-    const int64_t n_rows = FORM == SWIGLU ? p.N / 2 : p.N;       // output rows
+    const int n_rows = FORM == SWIGLU ? p.N / 2 : p.N;           // output rows
     const bool dense = p.idx == nullptr;
     int e = 0, members = 1, first = b;
     bool listed = false;
@@ -316,9 +340,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_nvfp4_gemv(const Params p, 
         if (e >= 0) {
             const bool mine = m0 + g < members;
             const int pair = mine ? pair_of(m0 + g) : 0;
-            const Set l[2] = {set_of(p, e, tile0, 0, n_rows),
-                              set_of(p, e, tile1, FORM == SWIGLU ? n_rows : 0, n_rows)};
-            dot_range<2>(ring, l, mine ? p.x + (int64_t)(pair / p.x_div) * p.ldx + 32 * t : nullptr, split, splits, chunks, p.K, acc);
+            const uint8_t *codes = p.codes + e * p.code_stride, *scales = p.scales + e * p.scale_stride;
+            const Set l[2] = {set_of(p, codes, scales, tile0, 0, n_rows),
+                              set_of(p, codes, scales, tile1, FORM == SWIGLU ? n_rows : 0, n_rows)};
+            dot_range<2>(ring, l, mine ? p.x + (int64_t)((uint32_t)pair * p.x_mul >> 16) * p.ldx : nullptr, split, splits,
+                         chunks, p.K, acc);
             coef = 512.0f * p.s_t[e];                            // the operands carry 2^-9
         }
         if (m0 > 0) __syncthreads();                             // the last pass's sums have been read
@@ -341,13 +367,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_nvfp4_gemv(const Params p, 
                     y[1] += part[w][1][rr][col];
                 }
                 if (FORM == SWIGLU) {
-                    const int64_t n = tile_row(orp, rr);
+                    const int n = tile_row(orp, rr);
                     if (n < n_rows)
                         reinterpret_cast<__nv_bfloat16 *>(p.out)[orow * p.ld_out + n] = __float2bfloat16_rn(silu(y[0]) * y[1]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int64_t n = tile_row(2 * orp + i, rr);
+                        const int n = tile_row(2 * orp + i, rr);
                         if (n < n_rows) reinterpret_cast<float *>(p.out)[orow * p.ld_out + n] = y[i];
                     }
                 }
@@ -365,7 +391,7 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
     __shared__ float part[COMBINE_WARPS][ROWS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int tile = blockIdx.y;
-    const int chunks = (int)((p.K + 127) / 128);
+    const int chunks = (p.K + 127) / 128;
     const bool dense = p.idx == nullptr;
     float tot[2] = {0, 0};
     const int units = p.k_r * chunks;
@@ -378,9 +404,9 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
         const int64_t pair = (int64_t)blockIdx.x * p.k_r + j;
         const int e = dense ? 0 : p.idx[pair];
         if (e >= 0 && e < p.E) {
-            const Set l[1] = {set_of(p, e, tile, 0, p.N)};
+            const Set l[1] = {set_of(p, p.codes + e * p.code_stride, p.scales + e * p.scale_stride, tile, 0, p.N)};
             float acc[1][4] = {{0, 0, 0, 0}};
-            dot_range<1>(ring, l, g == 0 ? p.x + pair * p.ldx + 32 * t : nullptr, ch, 1, ch_end, p.K, acc);
+            dot_range<1>(ring, l, g == 0 ? p.x + pair * p.ldx : nullptr, ch, 1, ch_end, p.K, acc);
             const float coef = 512.0f * (p.gate ? p.gate[pair] * p.s_t[e] : p.s_t[e]);
             tot[0] += coef * acc[0][0];                          // column 0 is lane t = 0's
             tot[1] += coef * acc[0][2];
@@ -393,7 +419,7 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
     }
     __syncthreads();
     if (threadIdx.x < ROWS) {
-        const int64_t n = tile_row(tile, threadIdx.x);
+        const int n = tile_row(tile, threadIdx.x);
         if (n < p.N) {
             float y = 0.0f;
 #pragma unroll
@@ -502,13 +528,16 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
         p.codes = codes_dev;
         p.scales = scales_dev;
         p.s_t = s_t_dev;
-        p.N = N;
-        p.K = K;
+        p.N = (int32_t)N;
+        p.K = (int32_t)K;
         p.E = E;
+        p.code_stride = N * (K / 2);
+        p.scale_stride = sf_bytes(N, K);
         p.idx = dense ? nullptr : expert_idx_dev + t0 * k_r;
         p.pairs = (int)(tn * k_r);
         p.k_r = k_r;
-        p.x_div = combine ? 1 : k_r;
+        // pair / k_r for pairs below MAX_PAIRS: exact because 1024 * 32 < 65536
+        p.x_mul = combine || k_r == 1 ? 65536u : 65536u / (uint32_t)k_r + 1u;
         p.gate = gate_dev ? gate_dev + t0 * k_r : nullptr;
         p.out = epilogue == MOE_EPI_SWIGLU_BF16
                     ? (void *)(reinterpret_cast<__nv_bfloat16 *>(out_dev) + t0 * k_r * ld_out)
