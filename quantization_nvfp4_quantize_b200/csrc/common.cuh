@@ -45,6 +45,15 @@ bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint
 nvfp4_status act8_expand(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, const int32_t *rows,
                          int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, cudaStream_t stream);
 
+// The launch attribute that goes with grid_wait().
+inline cudaLaunchAttribute overlap_attribute()
+{
+    cudaLaunchAttribute a = {};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    return a;
+}
+
 #define NVFP4_REQUIRE(cond, status, ...)                 \
     do {                                                 \
         if (!(cond)) return ::nvfp4::set_error(status, __VA_ARGS__); \
@@ -62,6 +71,14 @@ __host__ __device__ __forceinline__ int64_t sf_offset(int64_t r, int64_t c, int6
 __host__ __device__ __forceinline__ int64_t sf_bytes(int64_t rows, int64_t K) { return ((rows + 127) / 128) * 128 * (K / 16); }
 
 // ----------------------------------------------------------------- device side
+
+// A kernel launched with programmatic stream serialization starts while its
+// predecessor's last blocks still run: everything before grid_wait() touches no
+// global memory; grid_wait() returns when the predecessor has finished and its
+// writes are visible.  grid_release() lets the successor's blocks start once
+// every block of this grid has called it (they wait in grid_wait() themselves).
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }

@@ -281,6 +281,8 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_nvfp4_gemv(const Params p, 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int chunks = (p.K + 127) / 128;
     const int b = (int)blockIdx.x;
+    grid_wait();
+    grid_release();
     const int per_block = WARPS / splits;                        // row pairs
     const int rp = (int)blockIdx.y * per_block + warp / splits;  // this warp's
     const int split = warp % splits;
@@ -393,6 +395,8 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
     const int tile = blockIdx.y;
     const int chunks = (p.K + 127) / 128;
     const bool dense = p.idx == nullptr;
+    grid_wait();
+    grid_release();
     float tot[2] = {0, 0};
     const int units = p.k_r * chunks;
     const int per = (units + COMBINE_WARPS - 1) / COMBINE_WARPS;
@@ -436,6 +440,8 @@ __global__ void __launch_bounds__(THREADS) k_gemv_combine(const float *__restric
 {
     const int64_t n = (int64_t)blockIdx.x * THREADS + threadIdx.x;
     const int64_t t = blockIdx.y;
+    grid_wait();
+    grid_release();
     if (n >= N) return;
     float s = 0.0f;
     for (int j = 0; j < k_r; ++j) s += (gate ? gate[t * k_r + j] : 1.0f) * y[(t * k_r + j) * N + n];
@@ -453,6 +459,20 @@ static nvfp4_status allow_ring(size_t bytes)
     std::call_once(once[dev], [&] { err[dev] = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
     if (err[dev] != cudaSuccess) return set_error(NVFP4_ERR_CUDA, "k_nvfp4_gemv: smem attribute: %s", cudaGetErrorString(err[dev]));
     return NVFP4_OK;
+}
+
+template <typename... Params, typename... Args>
+static void launch(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args)
+{
+    cudaLaunchAttribute attr[1] = {overlap_attribute()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
 // Column splits of a row pair: the fewest that give every SM two blocks (or one
@@ -553,19 +573,19 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
                                                             : allow_ring<k_nvfp4_gemv<STORE>>(RING2);
         if (rc != NVFP4_OK) return rc;
         if (combine && need == 0) {
-            k_nvfp4_gemv_combine<<<dim3((unsigned)tn, (unsigned)tiles), 32 * COMBINE_WARPS, RING1, st>>>(p);
+            launch(k_nvfp4_gemv_combine, dim3((unsigned)tn, (unsigned)tiles), 32 * COMBINE_WARPS, RING1, st, p);
         } else if (combine) {
             float *out = reinterpret_cast<float *>(p.out);
             p.out = workspace;
             p.ld_out = N;
-            k_nvfp4_gemv<STORE><<<per_pair, THREADS, RING2, st>>>(p, splits);
+            launch(k_nvfp4_gemv<STORE>, per_pair, THREADS, RING2, st, p, splits);
             if (check_launch("k_nvfp4_gemv") != NVFP4_OK) return NVFP4_ERR_CUDA;
-            k_gemv_combine<<<dim3((unsigned)((N + THREADS - 1) / THREADS), (unsigned)tn), THREADS, 0, st>>>(
-                reinterpret_cast<const float *>(workspace), p.gate, tn, k_r, N, out, ld_out);
+            launch(k_gemv_combine, dim3((unsigned)((N + THREADS - 1) / THREADS), (unsigned)tn), THREADS, 0, st,
+                   reinterpret_cast<const float *>(workspace), p.gate, tn, (int)k_r, N, out, ld_out);
         } else if (epilogue == MOE_EPI_SWIGLU_BF16) {
-            k_nvfp4_gemv<SWIGLU><<<per_pair, THREADS, RING2, st>>>(p, splits);
+            launch(k_nvfp4_gemv<SWIGLU>, per_pair, THREADS, RING2, st, p, splits);
         } else {
-            k_nvfp4_gemv<STORE><<<per_pair, THREADS, RING2, st>>>(p, splits);
+            launch(k_nvfp4_gemv<STORE>, per_pair, THREADS, RING2, st, p, splits);
         }
         if (check_launch("k_nvfp4_gemv") != NVFP4_OK) return NVFP4_ERR_CUDA;
     }

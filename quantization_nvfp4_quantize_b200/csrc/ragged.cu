@@ -313,6 +313,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
         ptx::tmem_alloc_pair(ptx::smem_u32(&sh->tmem_base), TMEM_COLS);
         ptx::tmem_relinquish_pair();
     }
+    grid_wait();                           // the predecessor's results are visible from here on
     if (warp == FIX_WARP) {
         // lane l takes bounds 8l .. 8l + 7: running maximum, clamped to [0, M]
         // (a bad table can then give no row outside the tensors), and the
@@ -363,6 +364,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
         }
         if (lane == 31 && p.E == MAX_E) { sh->off[MAX_E] = last; sh->tiles[MAX_E] = incl; }
     }
+    grid_release();
     ptx::tc_fence_before();
     ptx::cluster_sync();                   // barriers of both CTAs initialized before any remote use
     ptx::tc_fence_after();
@@ -675,7 +677,7 @@ static nvfp4_status launch(const CUtensorMap &tm_m, const CUtensorMap &tm_n, con
     if (attr_err[dev] != cudaSuccess)
         return set_error(NVFP4_ERR_CUDA, "k_ragged_gemm: smem attribute: %s", cudaGetErrorString(attr_err[dev]));
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     const int64_t units = std::min<int64_t>(num_sms() / 2, max_tiles);
     cfg.gridDim = dim3((unsigned)(2 * units));
     cfg.blockDim = dim3(THREADS);
@@ -685,8 +687,9 @@ static nvfp4_status launch(const CUtensorMap &tm_m, const CUtensorMap &tm_n, con
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1] = overlap_attribute();
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     cudaLaunchKernelEx(&cfg, kern, tm_m, tm_n, p);
     return check_launch("k_ragged_gemm");
 }
