@@ -112,6 +112,8 @@ __global__ void __launch_bounds__(THREADS, QUANT_BLOCKS) k_act8_quantize(const _
                                                            int64_t ldx, uint8_t *__restrict__ codes, int64_t ldc,
                                                            uint8_t *__restrict__ scales, int64_t lds, int items)
 {
+    grid_wait();
+    grid_release();
     const int64_t first = (int64_t)blockIdx.x * THREADS + threadIdx.x;
     const int64_t stride = (int64_t)gridDim.x * THREADS;
     int64_t row = first / items;
@@ -156,6 +158,8 @@ __global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(con
                                                              int64_t M, int64_t K, __nv_bfloat16 *__restrict__ x,
                                                              int64_t ldx, int items)
 {
+    grid_wait();
+    grid_release();
     const int64_t first = (int64_t)blockIdx.x * THREADS + threadIdx.x;
     const int64_t stride = (int64_t)gridDim.x * THREADS;
     int64_t row = first / items;
@@ -225,6 +229,8 @@ __global__ void __launch_bounds__(THREADS, SWIGLU_BLOCKS) k_swiglu_act8(const __
                                                          uint8_t *__restrict__ scales, int64_t lds, int items,
                                                          int pad_bytes)
 {
+    grid_wait();
+    grid_release();
     const int64_t first = (int64_t)blockIdx.x * THREADS + threadIdx.x;
     const int64_t stride = (int64_t)gridDim.x * THREADS;
     int64_t row = first / items;
@@ -279,6 +285,8 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_BLOCKS) k_swiglu_act8_backwa
     __nv_bfloat16 *__restrict__ dy, int64_t lddy, __nv_bfloat16 *__restrict__ gh, int64_t ldgh,
     float *__restrict__ dgate)
 {
+    grid_wait();
+    grid_release();
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * (THREADS / 32);
     for (int64_t row = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5); row < M; row += warps) {
@@ -334,6 +342,8 @@ __global__ void __launch_bounds__(THREADS) k_combine_rows(const __nv_bfloat16 *_
                                                           const float *__restrict__ gate, int kr,
                                                           float *__restrict__ out, int64_t ldo)
 {
+    grid_wait();
+    grid_release();
     const int64_t t = blockIdx.x;
     const int64_t c = ((int64_t)blockIdx.y * THREADS + threadIdx.x) * 8;
     if (c >= H) return;
@@ -364,6 +374,8 @@ __global__ void __launch_bounds__(THREADS) k_route_backward(const int32_t *__res
                                                             const float *__restrict__ dgate_row, int64_t M, int64_t T,
                                                             int E, int kr, float *__restrict__ dlogits)
 {
+    grid_wait();
+    grid_release();
     const int lane = threadIdx.x & 31;
     const int64_t t = (int64_t)blockIdx.x * (THREADS / 32) + (threadIdx.x >> 5);
     if (t >= T) return;
@@ -405,8 +417,9 @@ nvfp4_status act8_expand(const uint8_t *codes, int64_t ldc, const uint8_t *scale
                          int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, cudaStream_t stream)
 {
     const int items = (int)((K + 15) / 16);
-    act8::k_act8_dequantize<<<act8::stream_blocks(M * items, act8::DEQUANT_BLOCKS), act8::THREADS, 0, stream>>>(
-        codes, ldc, scales, lds, rows, T, M, K, reinterpret_cast<__nv_bfloat16 *>(x), ldx, items);
+    launch_overlapped(act8::k_act8_dequantize, act8::stream_blocks(M * items, act8::DEQUANT_BLOCKS), act8::THREADS, 0,
+                      stream, codes, ldc, scales, lds, rows, T, M, K, reinterpret_cast<__nv_bfloat16 *>(x), ldx,
+                      items);
     return check_launch("k_act8_dequantize");
 }
 
@@ -431,8 +444,9 @@ extern "C" nvfp4_status act8_quantize(const void *x_dev, int64_t M, int64_t K, i
     NVFP4_REQUIRE(aligned16(x_dev) && aligned16(codes_dev) && aligned16(scales_dev), NVFP4_ERR_ALIGNMENT,
                   "act8_quantize: pointers must be 16-byte aligned");
     const int items = (int)((K + 127) / 128 * 8);
-    k_act8_quantize<<<stream_blocks(M * items, QUANT_BLOCKS), THREADS, 0, (cudaStream_t)stream>>>(
-        reinterpret_cast<const __nv_bfloat16 *>(x_dev), M, K, ldx, codes_dev, ld_codes, scales_dev, ld_scales, items);
+    launch_overlapped(k_act8_quantize, stream_blocks(M * items, QUANT_BLOCKS), THREADS, 0, (cudaStream_t)stream,
+                      reinterpret_cast<const __nv_bfloat16 *>(x_dev), M, K, ldx, codes_dev, ld_codes, scales_dev,
+                      ld_scales, items);
     return check_launch("k_act8_quantize");
 }
 
@@ -473,9 +487,10 @@ extern "C" nvfp4_status moe_swiglu_act8(const void *y_dev, int64_t M, int64_t I,
     NVFP4_REQUIRE(aligned16(y_dev) && aligned16(h_dev) && aligned16(codes_dev) && aligned16(scales_dev),
                   NVFP4_ERR_ALIGNMENT, "moe_swiglu_act8: pointers must be 16-byte aligned");
     const int items = (int)(I / 16);
-    k_swiglu_act8<<<stream_blocks(M * items, SWIGLU_BLOCKS), THREADS, 0, (cudaStream_t)stream>>>(
-        reinterpret_cast<const __nv_bfloat16 *>(y_dev), M, I, ldy, reinterpret_cast<__nv_bfloat16 *>(h_dev), ldh,
-        codes_dev, ld_codes, scales_dev, ld_scales, items, (int)(row_bytes - 2 * I / 32));
+    launch_overlapped(k_swiglu_act8, stream_blocks(M * items, SWIGLU_BLOCKS), THREADS, 0, (cudaStream_t)stream,
+                      reinterpret_cast<const __nv_bfloat16 *>(y_dev), M, I, ldy, reinterpret_cast<__nv_bfloat16
+                      *>(h_dev), ldh, codes_dev, ld_codes, scales_dev, ld_scales, items, (int)(row_bytes - 2 * I /
+                      32));
     return check_launch("k_swiglu_act8");
 }
 
@@ -505,10 +520,10 @@ extern "C" nvfp4_status moe_swiglu_act8_backward(const uint8_t *codes_dev, int64
     NVFP4_REQUIRE(aligned16(codes_dev) && aligned16(dh_dev) && aligned16(dy_dev) && aligned16(gh_dev),
                   NVFP4_ERR_ALIGNMENT, "moe_swiglu_act8_backward: pointers must be 16-byte aligned");
     const unsigned blocks = stream_blocks(M * 32, BACKWARD_BLOCKS);          // a warp per row
-    k_swiglu_act8_backward<<<blocks, THREADS, 0, (cudaStream_t)stream>>>(
-        codes_dev, ld_codes, scales_dev, ld_scales, reinterpret_cast<const __nv_bfloat16 *>(dh_dev), lddh, row_gate_dev,
-        M, I, reinterpret_cast<__nv_bfloat16 *>(dy_dev), lddy, reinterpret_cast<__nv_bfloat16 *>(gh_dev), ldgh,
-        dgate_dev);
+    launch_overlapped(k_swiglu_act8_backward, blocks, THREADS, 0, (cudaStream_t)stream, codes_dev, ld_codes,
+                      scales_dev, ld_scales, reinterpret_cast<const __nv_bfloat16 *>(dh_dev), lddh, row_gate_dev, M,
+                      I, reinterpret_cast<__nv_bfloat16 *>(dy_dev), lddy, reinterpret_cast<__nv_bfloat16 *>(gh_dev),
+                      ldgh, dgate_dev);
     return check_launch("k_swiglu_act8_backward");
 }
 
@@ -528,8 +543,8 @@ extern "C" nvfp4_status moe_combine_rows(const void *rows_dev, int64_t M, int64_
     NVFP4_REQUIRE(aligned16(rows_dev) && aligned16(out_dev), NVFP4_ERR_ALIGNMENT,
                   "moe_combine_rows: pointers must be 16-byte aligned");
     const dim3 grid((unsigned)T, (unsigned)((H + THREADS * 8 - 1) / (THREADS * 8)));
-    k_combine_rows<<<grid, THREADS, 0, (cudaStream_t)stream>>>(reinterpret_cast<const __nv_bfloat16 *>(rows_dev), M, H,
-                                                               ld_rows, dst_row_dev, gate_dev, k_r, out_dev, ld_out);
+    launch_overlapped(k_combine_rows, grid, THREADS, 0, (cudaStream_t)stream, reinterpret_cast<const __nv_bfloat16
+                      *>(rows_dev), M, H, ld_rows, dst_row_dev, gate_dev, k_r, out_dev, ld_out);
     return check_launch("k_combine_rows");
 }
 
@@ -544,7 +559,7 @@ extern "C" nvfp4_status moe_route_backward(const int32_t *topk_idx_dev, const fl
     NVFP4_REQUIRE(E >= 1 && E <= 65536 && k_r >= 1 && k_r <= 32 && T < (1ll << 31), NVFP4_ERR_UNSUPPORTED_SHAPE,
                   "moe_route_backward: need 1 <= E <= 65536, 1 <= k_r <= 32, T < 2^31");
     const unsigned blocks = (unsigned)((T + THREADS / 32 - 1) / (THREADS / 32));
-    k_route_backward<<<blocks, THREADS, 0, (cudaStream_t)stream>>>(topk_idx_dev, topk_gate_dev, dst_row_dev,
-                                                                   dgate_row_dev, M, T, E, k_r, dlogits_dev);
+    launch_overlapped(k_route_backward, blocks, THREADS, 0, (cudaStream_t)stream, topk_idx_dev, topk_gate_dev,
+                      dst_row_dev, dgate_row_dev, M, T, E, k_r, dlogits_dev);
     return check_launch("k_route_backward");
 }

@@ -54,6 +54,21 @@ inline cudaLaunchAttribute overlap_attribute()
     return a;
 }
 
+// Launch a kernel that calls grid_wait() (check_launch reports a failure).
+template <typename... Params, typename... Args>
+inline void launch_overlapped(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args)
+{
+    cudaLaunchAttribute attr[1] = {overlap_attribute()};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 #define NVFP4_REQUIRE(cond, status, ...)                 \
     do {                                                 \
         if (!(cond)) return ::nvfp4::set_error(status, __VA_ARGS__); \

@@ -461,20 +461,6 @@ static nvfp4_status allow_ring(size_t bytes)
     return NVFP4_OK;
 }
 
-template <typename... Params, typename... Args>
-static void launch(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t st, Args... args)
-{
-    cudaLaunchAttribute attr[1] = {overlap_attribute()};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 // Column splits of a row pair: the fewest that give every SM two blocks (or one
 // chunk of 128 columns per warp).
 static int column_splits(int64_t units, int64_t row_pairs, int64_t K)
@@ -573,19 +559,19 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
                                                             : allow_ring<k_nvfp4_gemv<STORE>>(RING2);
         if (rc != NVFP4_OK) return rc;
         if (combine && need == 0) {
-            launch(k_nvfp4_gemv_combine, dim3((unsigned)tn, (unsigned)tiles), 32 * COMBINE_WARPS, RING1, st, p);
+            launch_overlapped(k_nvfp4_gemv_combine, dim3((unsigned)tn, (unsigned)tiles), 32 * COMBINE_WARPS, RING1, st, p);
         } else if (combine) {
             float *out = reinterpret_cast<float *>(p.out);
             p.out = workspace;
             p.ld_out = N;
-            launch(k_nvfp4_gemv<STORE>, per_pair, THREADS, RING2, st, p, splits);
+            launch_overlapped(k_nvfp4_gemv<STORE>, per_pair, THREADS, RING2, st, p, splits);
             if (check_launch("k_nvfp4_gemv") != NVFP4_OK) return NVFP4_ERR_CUDA;
-            launch(k_gemv_combine, dim3((unsigned)((N + THREADS - 1) / THREADS), (unsigned)tn), THREADS, 0, st,
-                   reinterpret_cast<const float *>(workspace), p.gate, tn, (int)k_r, N, out, ld_out);
+            launch_overlapped(k_gemv_combine, dim3((unsigned)((N + THREADS - 1) / THREADS), (unsigned)tn), THREADS, 0, st,
+                              reinterpret_cast<const float *>(workspace), p.gate, tn, (int)k_r, N, out, ld_out);
         } else if (epilogue == MOE_EPI_SWIGLU_BF16) {
-            launch(k_nvfp4_gemv<SWIGLU>, per_pair, THREADS, RING2, st, p, splits);
+            launch_overlapped(k_nvfp4_gemv<SWIGLU>, per_pair, THREADS, RING2, st, p, splits);
         } else {
-            launch(k_nvfp4_gemv<STORE>, per_pair, THREADS, RING2, st, p, splits);
+            launch_overlapped(k_nvfp4_gemv<STORE>, per_pair, THREADS, RING2, st, p, splits);
         }
         if (check_launch("k_nvfp4_gemv") != NVFP4_OK) return NVFP4_ERR_CUDA;
     }

@@ -251,6 +251,19 @@ __device__ __forceinline__ void store_rows(const Params &p, float *out, int64_t 
         if (j < rows) *dst = ADD ? *dst + v[j] : v[j];
 }
 
+// n zeros from dst by `threads` threads, 16 bytes a store between the ends.
+template <typename T>
+__device__ __forceinline__ void zero_run(T *dst, int64_t n, int thread, int threads)
+{
+    const int64_t head = min(n, (int64_t)((16 - (reinterpret_cast<uintptr_t>(dst) & 15u)) & 15u) / (int64_t)sizeof(T));
+    const int64_t vecs = (n - head) * (int64_t)sizeof(T) / 16;
+    uint4 *body = reinterpret_cast<uint4 *>(dst + head);
+    for (int64_t i = thread; i < vecs; i += threads) body[i] = make_uint4(0, 0, 0, 0);
+    const int64_t done = head + vecs * (16 / (int64_t)sizeof(T));
+    for (int64_t i = thread; i < head; i += threads) dst[i] = T(0.0f);
+    for (int64_t i = done + thread; i < n; i += threads) dst[i] = T(0.0f);
+}
+
 // The same as bf16.  Neighbouring lanes exchange values: the even lane stores
 // row j, the odd lane row j + 1, both of columns m & ~1 and m | 1, so a store
 // instruction writes 2 rows x 64 bytes.
@@ -544,7 +557,20 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
             const Tile w = tile_at<MODE>(p, sh, t);
             const int64_t m = w.m0 + m_in_tile;
             if (MODE == WGRAD) {
-                if (ADD && w.stages == 0) continue;
+                if (w.stages == 0) {
+                    // an empty segment's gradient: its tiles share out the
+                    // expert's N x K zeros as one contiguous run
+                    if (!ADD) {
+                        const int64_t all = p.out_n * p.ld_out, per = (int64_t)p.m_tiles * p.n_tiles;
+                        const int64_t i = w.m0 / TILE * p.n_tiles + w.n0 / TILE;
+                        const int64_t share = ((all + per - 1) / per + 15) / 16 * 16;
+                        const int64_t lo = min(all, i * share), hi = min(all, lo + share);
+                        OutT *base = reinterpret_cast<OutT *>(p.out) + ((int64_t)w.split * p.E + w.e) * all;
+                        zero_run(base + lo, hi - lo, (int)rank * 32 * EPI_WARPS + (warp - EPI_WARP0) * 32 + lane,
+                                 2 * 32 * EPI_WARPS);
+                    }
+                    continue;
+                }
                 // row n of the gradient = TMEM column, its column k = lane
                 const int64_t n = w.n0 + half * 128;
                 const int64_t row = ((int64_t)w.split * p.E + w.e) * p.out_n + n;
@@ -574,31 +600,25 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 }
                 if (!ok) break;
                 const int acc = iter & 1;
-                if (w.stages > 0) {
-                    if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status))
-                        break;
-                    ++iter;
-                    ptx::tc_fence_after();
-                }
+                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status))
+                    break;
+                ++iter;
+                ptx::tc_fence_after();
                 // the last chunk's columns are stored as they are read: the stores
                 // drain while the next columns come
                 const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)half * 128 + ((uint32_t)(q * 32) << 16);
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     float y[32];
+                    uint32_t x[32];
+                    ptx::tmem_ld_32x32b_x32(src + c * 32, x);
+                    ptx::tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = v[c * 32 + i];
-                    if (w.stages > 0) {
-                        uint32_t x[32];
-                        ptx::tmem_ld_32x32b_x32(src + c * 32, x);
-                        ptx::tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) y[i] += __uint_as_float(x[i]);
-                        if (c == 3) {
-                            ptx::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
-                        }
+                    for (int i = 0; i < 32; ++i) y[i] = v[c * 32 + i] + __uint_as_float(x[i]);
+                    if (c == 3) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
                     }
                     store_rows<ADD>(p, reinterpret_cast<OutT *>(p.out), row + c * 32, rows - c * 32, m, y);
                     __syncwarp();                        // lanes without an output rejoin before the collective load
@@ -647,6 +667,8 @@ __global__ void __launch_bounds__(256) k_wgrad_reduce(const float *__restrict__ 
                                                       int out_f32, int accumulate)
 {
     const int64_t stride = (int64_t)gridDim.x * 256;
+    grid_wait();
+    grid_release();
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += stride) {
         float s = 0.0f;
         for (int k = 0; k < splits; ++k) s += part[(int64_t)k * n + i];
@@ -857,7 +879,7 @@ extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t
     if (rc != NVFP4_OK) return rc;
     const int64_t n = (int64_t)E * N * K;
     const unsigned blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, (int64_t)num_sms() * 8));
-    k_wgrad_reduce<<<blocks, 256, 0, st>>>(reinterpret_cast<const float *>(partials), splits, n, out_dev,
-                                           out_f32 ? 1 : 0, accumulate ? 1 : 0);
+    launch_overlapped(k_wgrad_reduce, dim3(blocks), 256, 0, st, reinterpret_cast<const float *>(partials), splits, n, out_dev,
+                      out_f32 ? 1 : 0, accumulate ? 1 : 0);
     return check_launch("k_wgrad_reduce");
 }
