@@ -3,12 +3,18 @@
 //
 //   y[r, n] = s_t[e] * sum_k e2m1(w_e[n,k]) sf_e[n, k/16] x[r, k]
 //
-// Bound by HBM: 0.5625 bytes per weight, each read once; a token's rows of x
-// stay in L1.  To keep up with HBM (about 41 weights per clock and SM) the
-// decode has to cost about two instructions per weight, so the multiply-adds
-// go to mma.sync (m16n8k16, BF16, f32 accumulation): 16 weight rows times up
-// to 8 tokens per instruction.  A single token uses one of the 8 columns;
-// the tensor pipe is idle otherwise.
+// The floor is HBM (0.5625 bytes per weight, each read once: 41 weights per
+// clock and SM); what bounds it is the decode.  A weight costs 3.9
+// thread-instructions in all (1.0 mask, 0.9 shift, 0.6 scale, 0.13 MMA, the rest
+// copies, x and addresses), the ALU pipe's share of them half of its time at the
+// HBM rate and the whole issue 1.2 times it: 82 experts of 4096 x 1536 (16
+// tokens, top-8 of 128) take 104 us against 45 for the bytes.
+// The multiply-adds go to mma.sync (m16n8k16, BF16, f32 accumulation), 16
+// weight rows times up to 8 tokens per instruction: the tensor pipe is idle
+// otherwise (13% with them), and a second token costs no decode.  Measured
+// slower: more warps per SM (spills at 80 registers; 96 registers the same),
+// shifts written as multiplications, operands prefetched in registers instead
+// of per-lane shared slots.
 //
 // Decode: a nibble's bits s|ee|m land in a BF16's sign, low exponent and top
 // mantissa bits, which reads as e2m1 * 2^-126 (its subnormal included); one
@@ -39,7 +45,7 @@ constexpr int ROWS = 16;                 // weight rows of a set
 constexpr int COLS = 8;                  // tokens per MMA
 
 constexpr int BLOCKS = 4;                // resident per SM
-constexpr int DEPTH = 4;                 // ring slots per warp: one chunk computed, DEPTH - 1 in flight
+constexpr int DEPTH = 3;                 // ring slots per warp: one chunk computed, DEPTH - 1 in flight
 constexpr int MAX_PAIRS = 1024;          // (token, slot) pairs per launch
 
 enum Form { STORE = 0, SWIGLU = 1 };
@@ -176,9 +182,9 @@ __device__ __forceinline__ void copy4(void *dst, const void *src)
 
 // Chunks of 128 columns ch0, ch0 + stride, ... below `chunks`, of SETS row sets
 // against the same x; DEPTH - 1 chunks are in flight while one is computed.
-// x: the lane's token row, or null (zeros).  K is a multiple of 64, so half of
-// the last chunk may be missing: its lanes read earlier columns again, against
-// zeros of x.
+// x: the lane's token row (a column without a token may take any row: its sums
+// are not stored).  K is a multiple of 64, so half of the last chunk may be
+// missing: its lanes read earlier columns again, against zeros of x.
 template <int SETS>
 __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS], const __nv_bfloat16 *x, int ch0,
                                           int stride, int chunks, int K, float (&acc)[SETS][4])
@@ -218,26 +224,16 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    uint4 v[4];                          // zeros where the lane has no token
-#pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
-    int xcol = ch0 * 128 + 32 * t;
+    uint4 v[4];
+    const __nv_bfloat16 *px = x + at;
     auto load_x = [&]() {
-        if (x != nullptr) {
-            if (xcol < K) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(x + xcol);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = __ldg(src + k);
-            } else {                     // past the end, or the missing half of the last chunk
-#pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] = make_uint4(0, 0, 0, 0);
-            }
-            xcol += step;
-        }
+        for (int k = 0; k < 4; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(px) + k);
     };
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i) issue();
     load_x();
+    int xcol = ch0 * 128 + 32 * t;                                // of the chunk whose x is in v
     for (int i = 0; i < n; ++i) {
         issue();
         uint32_t xp[16];
@@ -248,7 +244,17 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
             xp[4 * q + 2] = __byte_perm(v[q].y, v[q].w, 0x5410);
             xp[4 * q + 3] = __byte_perm(v[q].y, v[q].w, 0x7632);
         }
-        load_x();
+        if (i + 1 == n && (K & 64)) {
+            // the last chunk may be the half one (uniform branch; full lanes keep theirs)
+            const uint32_t keep = xcol < K ? 0xFFFFFFFFu : 0u;
+#pragma unroll
+            for (int q = 0; q < 16; ++q) xp[q] &= keep;
+        }
+        if (i + 1 < n) {
+            xcol += step;
+            if (xcol < K) px += step;
+            load_x();
+        }
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
         const Slot<SETS> &slot = ring[i % DEPTH];
 #pragma unroll
@@ -340,13 +346,11 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_nvfp4_gemv(const Params p, 
         float acc[2][4] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
         float coef = 0.0f;
         if (e >= 0) {
-            const bool mine = m0 + g < members;
-            const int pair = mine ? pair_of(m0 + g) : 0;
+            const int pair = pair_of(min(m0 + g, members - 1));
             const uint8_t *codes = p.codes + e * p.code_stride, *scales = p.scales + e * p.scale_stride;
             const Set l[2] = {set_of(p, codes, scales, tile0, 0, n_rows),
                               set_of(p, codes, scales, tile1, FORM == SWIGLU ? n_rows : 0, n_rows)};
-            dot_range<2>(ring, l, mine ? p.x + (int64_t)((uint32_t)pair * p.x_mul >> 16) * p.ldx : nullptr, split, splits,
-                         chunks, p.K, acc);
+            dot_range<2>(ring, l, p.x + (int64_t)((uint32_t)pair * p.x_mul >> 16) * p.ldx, split, splits, chunks, p.K, acc);
             coef = 512.0f * p.s_t[e];                            // the operands carry 2^-9
         }
         if (m0 > 0) __syncthreads();                             // the last pass's sums have been read
@@ -410,7 +414,7 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
         if (e >= 0 && e < p.E) {
             const Set l[1] = {set_of(p, p.codes + e * p.code_stride, p.scales + e * p.scale_stride, tile, 0, p.N)};
             float acc[1][4] = {{0, 0, 0, 0}};
-            dot_range<1>(ring, l, g == 0 ? p.x + pair * p.ldx : nullptr, ch, 1, ch_end, p.K, acc);
+            dot_range<1>(ring, l, p.x + pair * p.ldx, ch, 1, ch_end, p.K, acc);
             const float coef = 512.0f * (p.gate ? p.gate[pair] * p.s_t[e] : p.s_t[e]);
             tot[0] += coef * acc[0][0];                          // column 0 is lane t = 0's
             tot[1] += coef * acc[0][2];
