@@ -657,6 +657,15 @@ NVFP4_API nvfp4_status nvfp4_debug_gemm_wait_expiry(
     const int32_t *offsets_dev, int32_t epilogue, const int32_t *row_token_dev, const float *row_gate_dev,
     void *out_dev, int64_t ld_out, int32_t *dev_status, int64_t wait_limit_ns, void *stream);
 
+/* nvfp4_debug_ragged_wait_expiry -- the same for moe_ragged_gemm's CTA pairs:
+ * one expert, one tile (M, N <= 256, f32 out), whose "accumulator ready" is
+ * withheld.  Both CTAs' epilogues run out, nothing is written, *dev_status =
+ * NVFP4_ERR_TIMEOUT and the context stays usable. */
+NVFP4_API nvfp4_status nvfp4_debug_ragged_wait_expiry(const void *a_dev, int64_t lda, int64_t M, const void *w_dev,
+                                                      int64_t N, int64_t K, const int32_t *offsets_dev, void *out_dev,
+                                                      int64_t ld_out, int32_t *dev_status, int64_t wait_limit_ns,
+                                                      void *stream);
+
 /* --------------------------------------------------------------------------
  * nvfp4_debug_encode -- runs the library's element and scale encoders on n
  * arbitrary floats (for validation against an independent definition):

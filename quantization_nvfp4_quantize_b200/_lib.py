@@ -90,6 +90,8 @@ SIGNATURES = {
     "moe_nvfp4_gemv": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_int64, c_int32,
                                  c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_int64, c_void_p, c_size_t,
                                  c_void_p]),
+    "nvfp4_debug_ragged_wait_expiry": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
+                                                 c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
     "nvfp4_debug_gemm_wait_expiry": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                                c_int64, c_int64, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
                                                c_void_p, c_int64, c_void_p, c_int64, c_void_p]),

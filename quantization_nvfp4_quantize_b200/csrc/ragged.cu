@@ -104,6 +104,8 @@ struct Params {
     int64_t ld_out;
     int pairs;                 // bf16 out: two neighbouring columns may be stored at once
     int32_t *dev_status;
+    uint64_t wait_limit_ns;    // bound of every mbarrier wait
+    int withhold;              // test hook: the first tile's "accumulator ready" is not signalled
 };
 
 struct Shared {
@@ -121,7 +123,7 @@ struct Shared {
 
 // A converged warp's wait, bounded: false on a timeout or another role's.
 // `cluster`: the peer CTA's threads wrote shared memory before they arrived.
-__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *dev_status,
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, const Params &p,
                                          bool ignore_abort = false, bool cluster = false)
 {
     bool ok = true;
@@ -132,9 +134,9 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
             if (!ignore_abort && *abort_flag) { ok = false; break; }
             const uint64_t now = globaltimer_ns();
             if (t0 == 0) t0 = now;
-            else if (now - t0 > TIMEOUT_NS) {
+            else if (now - t0 > p.wait_limit_ns) {
                 *abort_flag = 1;
-                report_status(dev_status, NVFP4_ERR_TIMEOUT);
+                report_status(p.dev_status, NVFP4_ERR_TIMEOUT);
                 ok = false;
                 break;
             }
@@ -403,9 +405,9 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 // this CTA's half of the operand
                 const int half_n = w.nt / 2;
                 const int mn = (int)(m_side ? w.m0 + rank * 128 : w.n0 + (int)rank * half_n);
-                                const uint32_t bytes = m_side || MODE == WGRAD ? OPER_BYTES : (uint32_t)half_n * (BK * 2);
+                const uint32_t bytes = m_side || MODE == WGRAD ? OPER_BYTES : (uint32_t)half_n * (BK * 2);
                 for (int kb = 0; kb < w.stages; ++kb) {
-                    if (!wait_bar(ptx::smem_u32(&sh->empty[stage]), phase ^ 1u, abort_flag, p.dev_status)) {
+                    if (!wait_bar(ptx::smem_u32(&sh->empty[stage]), phase ^ 1u, abort_flag, p)) {
                         ok = false;
                         break;
                     }
@@ -470,8 +472,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 const int64_t len = MODE == WGRAD ? (int64_t)(w.r1 - w.r0) : p.red;
                 for (int kb = 0; kb < w.stages;) {
                     const int acc = iter & 1;
-                    if (!wait_bar(ptx::smem_u32(&sh->tmem_empty[acc]), (uint32_t)((iter >> 1) & 1) ^ 1u, abort_flag,
-                                  p.dev_status)) {
+                    if (!wait_bar(ptx::smem_u32(&sh->tmem_empty[acc]), (uint32_t)((iter >> 1) & 1) ^ 1u, abort_flag, p)) {
                         ok = false;
                         break;
                     }
@@ -480,7 +481,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     const uint32_t d = tmem + (uint32_t)acc * TILE;
                     const int kend = min(kb + w.chunk, w.stages);
                     for (uint32_t first = 1; kb < kend; ++kb, first = 0) {
-                        if (!ready && !wait_bar(full0 + 8 * stage, phase, abort_flag, p.dev_status, false, MODE == WGRAD)) {
+                        if (!ready && !wait_bar(full0 + 8 * stage, phase, abort_flag, p, false, MODE == WGRAD)) {
                             ok = false;
                             break;
                         }
@@ -508,6 +509,14 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                         issued = true;
                     }
                     if (!ok) break;
+                    if (MODE == FWD && p.withhold) {
+                        // test hook: the epilogue's wait runs out; the MMAs are drained
+                        // here, before any thread can release TMEM
+                        if (one) ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->drain), 1);
+                        wait_bar(ptx::smem_u32(&sh->drain), 0, abort_flag, p, true);
+                        issued = ok = false;
+                        break;
+                    }
                     if (one) ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->tmem_full[acc]), 3);
                     __syncwarp();
                 }
@@ -515,7 +524,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
             if (!ok && issued) {
                 // let every issued MMA finish before TMEM is released
                 if (one) ptx::tc_commit_pair_mc(ptx::smem_u32(&sh->drain), 1);
-                wait_bar(ptx::smem_u32(&sh->drain), 0, abort_flag, p.dev_status, true);
+                wait_bar(ptx::smem_u32(&sh->drain), 0, abort_flag, p, true);
             }
         }
         __syncwarp();
@@ -531,7 +540,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 stage = (s + 1) % STAGES;
                 const int rows = (w.r1 - w.r0) - (w.stages - 1) * BK;
                 if (rows == BK) continue;
-                if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p.dev_status)) break;
+                if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p)) break;
                 parity ^= 1u << s;
                 uint8_t *base = stage_base + s * STAGE_BYTES;
                 // 128-byte rows `rows`..63 of both operands' boxes; the swizzle stays inside a row
@@ -581,7 +590,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 bool ok = true;
                 for (int kb = w.chunk; kb < w.stages; kb += w.chunk, ++iter) {       // all chunks but the last
                     const int acc = iter & 1;
-                    ok = wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status);
+                    ok = wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p);
                     if (!ok) break;
                     ptx::tc_fence_after();
                     const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)half * 128 + ((uint32_t)(q * 32) << 16);
@@ -600,7 +609,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 }
                 if (!ok) break;
                 const int acc = iter & 1;
-                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status))
+                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p))
                     break;
                 ++iter;
                 ptx::tc_fence_after();
@@ -625,7 +634,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 }
             } else {
                 const int acc = iter & 1;
-                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p.dev_status))
+                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p))
                     break;
                 ++iter;
                 ptx::tc_fence_after();
@@ -734,10 +743,9 @@ static int wgrad_splits(int64_t M, int64_t N, int64_t K, int32_t E)
 
 using namespace nvfp4;
 
-extern "C" nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t M, const void *w_dev, int64_t N,
-                                        int64_t K, int32_t E, const int32_t *offsets_dev, int32_t transpose,
-                                        void *out_dev, int64_t ld_out, int32_t out_f32, int32_t *dev_status,
-                                        void *stream)
+static nvfp4_status ragged_gemm(const void *a_dev, int64_t lda, int64_t M, const void *w_dev, int64_t N, int64_t K,
+                                int32_t E, const int32_t *offsets_dev, int32_t transpose, void *out_dev, int64_t ld_out,
+                                int32_t out_f32, int32_t *dev_status, void *stream, uint64_t wait_limit_ns, int withhold)
 {
     using namespace nvfp4::ragged;
     NVFP4_REQUIRE(M >= 0 && N >= 0 && K >= 0, NVFP4_ERR_INVALID_ARG, "moe_ragged_gemm: negative size");
@@ -768,6 +776,8 @@ extern "C" nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t 
     p.E = E;
     p.m_tiles = (int)((outw + TILE - 1) / TILE);
     p.splits = 1;
+    p.wait_limit_ns = wait_limit_ns;
+    p.withhold = withhold;
     p.offsets = offsets_dev;
     p.out = out_dev;
     p.ld_out = ld_out;
@@ -782,6 +792,28 @@ extern "C" nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t 
                        : launch<DGRAD, __nv_bfloat16, false>(tm_m, tm_n, p, max_tiles, st);
     return out_f32 ? launch<FWD, float, false>(tm_m, tm_n, p, max_tiles, st)
                    : launch<FWD, __nv_bfloat16, false>(tm_m, tm_n, p, max_tiles, st);
+}
+
+extern "C" nvfp4_status moe_ragged_gemm(const void *a_dev, int64_t lda, int64_t M, const void *w_dev, int64_t N,
+                                        int64_t K, int32_t E, const int32_t *offsets_dev, int32_t transpose,
+                                        void *out_dev, int64_t ld_out, int32_t out_f32, int32_t *dev_status,
+                                        void *stream)
+{
+    return ragged_gemm(a_dev, lda, M, w_dev, N, K, E, offsets_dev, transpose, out_dev, ld_out, out_f32, dev_status, stream,
+                       nvfp4::ragged::TIMEOUT_NS, 0);
+}
+
+extern "C" nvfp4_status nvfp4_debug_ragged_wait_expiry(const void *a_dev, int64_t lda, int64_t M, const void *w_dev,
+                                                       int64_t N, int64_t K, const int32_t *offsets_dev, void *out_dev,
+                                                       int64_t ld_out, int32_t *dev_status, int64_t wait_limit_ns,
+                                                       void *stream)
+{
+    NVFP4_REQUIRE(dev_status && wait_limit_ns >= 1000000 && wait_limit_ns <= 1000000000ll, NVFP4_ERR_INVALID_ARG,
+                  "nvfp4_debug_ragged_wait_expiry: needs dev_status and 1 ms <= wait_limit_ns <= 1 s");
+    NVFP4_REQUIRE(M >= 1 && M <= nvfp4::ragged::TILE && N >= 1 && N <= nvfp4::ragged::TILE, NVFP4_ERR_UNSUPPORTED_SHAPE,
+                  "nvfp4_debug_ragged_wait_expiry: one tile (M, N <= 256)");
+    return ragged_gemm(a_dev, lda, M, w_dev, N, K, 1, offsets_dev, 0, out_dev, ld_out, 1, dev_status, stream,
+                       (uint64_t)wait_limit_ns, 1);
 }
 
 // Workspace of a weight gradient: [BF16 copy of the kept rows][partial results].
@@ -863,6 +895,7 @@ extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t
     p.m_tiles = (int)((K + TILE - 1) / TILE);
     p.n_tiles = (int)((N + TILE - 1) / TILE);
     p.splits = splits;
+    p.wait_limit_ns = TIMEOUT_NS;
     p.offsets = offsets_dev;
     p.out = splits > 1 ? partials : out_dev;
     p.ld_out = K;

@@ -346,3 +346,22 @@ def test_gradients_match_differences(cuda):
         bw = float((sum_bound(66, 65 * c.double().abs().max() * a.double().abs().max()) * v.abs()).sum())
         assert abs(float((da * u).sum()) - fa) <= ba + 1e-6
         assert abs(float((dw * v).sum()) - fw) <= bw + 1e-6
+
+
+def test_bounded_wait_expiry_reports_timeout(cuda):
+    """The pair's epilogues wait for a signal that never comes: the bound ends
+    them, the status says so, nothing is written, and the next call is right."""
+    from quantization_nvfp4_quantize_b200 import _lib
+    lib = _lib.load()
+    a, w, off = rnd(70, 100, 128), rnd(71, 1, 200, 128), offsets_of([100], cuda)
+    out = torch.full((100, 200), 3.0, device=cuda)
+    status = torch.zeros(1, dtype=I32, device=cuda)
+    p = api._p
+    st = lib.nvfp4_debug_ragged_wait_expiry(p(a), 128, 100, p(w), 200, 128, p(off), p(out), 200, p(status), 20_000_000,
+                                            api._stream(cuda))
+    assert st == 0
+    torch.cuda.synchronize()
+    assert api.read_status(status) == 5 and bool((out == 3).all())
+    got = api.ragged_gemm(a, w, off, out_dtype=F32)
+    y, s = ref_rows(a, w, off, False, torch.zeros(100, 200, device=cuda))
+    check(got, y, sum_bound(128, s) + rounding(F32, y))

@@ -40,6 +40,14 @@ def test_ragged_gemm():
     assert lib.moe_ragged_gemm(*back) == 0
 
 
+def test_ragged_wait_expiry_arguments():
+    #       a     lda  M    w     N    K   off   out   ld   stat  limit    stream
+    good = [FAKE, 64, 100, FAKE, 128, 64, FAKE, FAKE, 128, FAKE, 2000000, None]
+    calls("nvfp4_debug_ragged_wait_expiry", good, [
+        (9, None, INVALID), (10, 999999, INVALID), (10, 1000000001, INVALID), (2, 257, SHAPE), (4, 257, SHAPE),
+        (2, 0, SHAPE), (0, None, INVALID)])
+
+
 def test_ragged_wgrad():
     #       g     ldg  M    a     lda asc   lds rows  T   N    K   E  off   out   f32 acc ws  n  stat  stream
     good = [FAKE, 256, 5000, FAKE, 256, None, 0, None, 0, 256, 256, 128, FAKE, FAKE, 1, 0, None, 0, None, None]
