@@ -86,6 +86,7 @@ constexpr int EPI_WARPS = 8, EPI_WARP0 = 4;
 constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
 constexpr int PROD_M_WARP = 0, MMA_WARP = 1, PROD_N_WARP = 2, FIX_WARP = 3;
 constexpr uint32_t TMEM_COLS = 512;
+constexpr int COLS = 16;                         // accumulator columns read at a time
 constexpr int MAX_E = 256;
 constexpr uint64_t TIMEOUT_NS = 1000000000ull;
 
@@ -145,6 +146,49 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     return __all_sync(0xffffffffu, ok ? 1 : 0) != 0;         // a uniform answer
 }
 
+// A unit's tiles t = unit, unit + n_units, ...  WGRAD keeps t's digits (expert,
+// split, N tile, M tile) and adds n_units digit by digit: a division costs a
+// role ~200 clk per tile, and there were five.  The M tiles run innermost: the
+// units then write whole output rows together (32 experts of 4096 x 1536:
+// 391 us -> 376 us).
+template <int MODE>
+struct Walk {
+    int t;
+    int e, split, nt, mt;
+    int de, ds, dn, dm;
+
+    __device__ __forceinline__ static void digits(const Params &p, int v, int &e, int &s, int &m, int &n)
+    {
+        const int mn = p.m_tiles * p.n_tiles, per = mn * p.splits;
+        e = v / per;
+        v -= e * per;
+        s = v / mn;
+        v -= s * mn;
+        n = v / p.m_tiles;
+        m = v - n * p.m_tiles;
+    }
+    __device__ __forceinline__ Walk(const Params &p, int unit, int n_units) : t(unit)
+    {
+        if (MODE == WGRAD) {
+            digits(p, unit, e, split, mt, nt);
+            digits(p, n_units, de, ds, dm, dn);
+        }
+    }
+    __device__ __forceinline__ void next(const Params &p, int n_units)
+    {
+        t += n_units;
+        if (MODE == WGRAD) {
+            nt += dn;
+            mt += dm;
+            split += ds;
+            e += de;
+            if (mt >= p.m_tiles) { mt -= p.m_tiles; ++nt; }
+            if (nt >= p.n_tiles) { nt -= p.n_tiles; ++split; }
+            if (split >= p.splits) { split -= p.splits; ++e; }
+        }
+    }
+};
+
 // What a tile covers.
 struct Tile {
     int e;
@@ -157,71 +201,61 @@ struct Tile {
     int split;
 };
 
+// Values from shared memory are broadcast, so that the compiler knows
+// everything here to be the same in all lanes.
 template <int MODE>
-__device__ __forceinline__ Tile tile_of(const Params &p, const Shared *sh, int t)
+__device__ __forceinline__ Tile tile_at(const Params &p, const Shared *sh, const Walk<MODE> &at)
 {
+    const auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     Tile w;
     if (MODE == WGRAD) {
-        const int per = p.m_tiles * p.n_tiles * p.splits;
-        w.e = t / per;
-        int rem = t - w.e * per;
-        w.split = rem / (p.m_tiles * p.n_tiles);
-        rem -= w.split * (p.m_tiles * p.n_tiles);
-        const int mt = rem / p.n_tiles;
-        w.m0 = (int64_t)mt * TILE;
-        w.n0 = (int64_t)(rem - mt * p.n_tiles) * TILE;
+        w.e = at.e;
+        w.split = at.split;
+        w.m0 = (int64_t)at.mt * TILE;
+        w.n0 = (int64_t)at.nt * TILE;
         w.n_end = p.out_n;
         w.nt = TILE;
-        const int lo = sh->off[w.e], hi = sh->off[w.e + 1];
-        // whole stages per split, so that only a segment's last stage is ragged
-        const int chunk = ((hi - lo + p.splits - 1) / p.splits + BK - 1) / BK * BK;
-        const int64_t r0 = (int64_t)lo + (int64_t)w.split * chunk;
-        w.r0 = (int)min((int64_t)hi, r0);
-        w.r1 = (int)min((int64_t)hi, r0 + chunk);
+        w.r0 = same(sh->off[w.e]);
+        w.r1 = same(sh->off[w.e + 1]);
+        if (p.splits > 1) {
+            // whole stages per split, so that only a segment's last stage is ragged
+            const int rows = ((w.r1 - w.r0 + p.splits - 1) / p.splits + BK - 1) / BK * BK;
+            const int64_t r0 = (int64_t)w.r0 + (int64_t)w.split * rows;
+            w.r0 = (int)min((int64_t)w.r1, r0);
+            w.r1 = (int)min((int64_t)w.r1, r0 + rows);
+        }
         w.stages = (w.r1 - w.r0 + BK - 1) / BK;
-        const int chunks = max(1, (w.stages + CHUNK - 1) / CHUNK);
-        w.chunk = max(1, (w.stages + chunks - 1) / chunks);
+        w.chunk = max(1, w.stages);
+        if (w.stages > CHUNK) {
+            const int chunks = (w.stages + CHUNK - 1) / CHUNK;
+            w.chunk = (w.stages + chunks - 1) / chunks;
+        }
     } else {
-        const int rt = t / p.m_tiles;
-        int lo = 0, hi = p.E;                        // tiles[lo] <= rt < tiles[hi]
+        int lo = 0, hi = p.E;                        // expert: tiles[lo] * m_tiles <= t < tiles[hi] * m_tiles
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (sh->tiles[mid] <= rt) lo = mid; else hi = mid;
+            if (same(sh->tiles[mid]) * p.m_tiles <= at.t) lo = mid; else hi = mid;
         }
         // an expert's tiles: its row tiles innermost, they share a weight tile
-        const int row_tiles = sh->tiles[lo + 1] - sh->tiles[lo];
-        const int idx = t - sh->tiles[lo] * p.m_tiles;
-        const int mt = idx / row_tiles, i = idx - mt * row_tiles;
-        const int len = sh->off[lo + 1] - sh->off[lo];
-        const int size = ((len + row_tiles - 1) / row_tiles + N_STEP - 1) / N_STEP * N_STEP;
+        const int first = same(sh->tiles[lo]), row_tiles = same(sh->tiles[lo + 1]) - first;
+        const int off = same(sh->off[lo]), end = same(sh->off[lo + 1]);
+        int mt = at.t - first * p.m_tiles, i = 0, size = end - off;
+        if (row_tiles > 1) {
+            const int idx = mt;
+            mt = idx / row_tiles;
+            i = idx - mt * row_tiles;
+            size = (size + row_tiles - 1) / row_tiles;
+        }
+        size = (size + N_STEP - 1) / N_STEP * N_STEP;
         w.e = lo;
         w.m0 = (int64_t)mt * TILE;
-        w.n0 = (int64_t)sh->off[lo] + (int64_t)i * size;
-        w.n_end = sh->off[lo + 1];
+        w.n0 = (int64_t)off + (int64_t)i * size;
+        w.n_end = end;
         w.nt = min(size, (int)((w.n_end - w.n0 + N_STEP - 1) / N_STEP) * N_STEP);
         w.r0 = w.r1 = 0;
         w.split = 0;
         w.stages = w.chunk = (int)((p.red + BK - 1) / BK);
     }
-    return w;
-}
-
-// tile_of with every field broadcast, so that the compiler knows it to be the
-// same in all lanes.
-template <int MODE>
-__device__ __forceinline__ Tile tile_at(const Params &p, const Shared *sh, int t)
-{
-    Tile w = tile_of<MODE>(p, sh, t);
-    w.e = __shfl_sync(0xffffffffu, w.e, 0);
-    w.m0 = __shfl_sync(0xffffffffu, w.m0, 0);
-    w.n0 = __shfl_sync(0xffffffffu, w.n0, 0);
-    w.n_end = __shfl_sync(0xffffffffu, w.n_end, 0);
-    w.nt = __shfl_sync(0xffffffffu, w.nt, 0);
-    w.r0 = __shfl_sync(0xffffffffu, w.r0, 0);
-    w.r1 = __shfl_sync(0xffffffffu, w.r1, 0);
-    w.stages = __shfl_sync(0xffffffffu, w.stages, 0);
-    w.chunk = __shfl_sync(0xffffffffu, w.chunk, 0);
-    w.split = __shfl_sync(0xffffffffu, w.split, 0);
     return w;
 }
 
@@ -240,17 +274,22 @@ __device__ __forceinline__ void take_registers()
     if (MODE == WGRAD) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
 }
 
-// 32 output rows from `row`, of which `rows` exist, at column m = this lane's.
-// ADD: to the old value, in f32.
-template <bool ADD>
+// R output rows from `row`, of which `rows` exist, at column m = this lane's.
+// ADD: to the old value, in f32.  The f32 stores are marked streaming: nothing
+// here reads them again, the operands' tiles are (WGRAD, 1536 x 2048, 128
+// segments of 256 rows: 398 -> 382 us).
+template <bool ADD, int R>
 __device__ __forceinline__ void store_rows(const Params &p, float *out, int64_t row, int rows, int64_t m,
-                                           const float (&v)[32])
+                                           const float (&v)[R])
 {
     float *dst = out + row * p.ld_out + m;
     if (m >= p.out_m) rows = 0;
 #pragma unroll
-    for (int j = 0; j < 32; ++j, dst += p.ld_out)
-        if (j < rows) *dst = ADD ? *dst + v[j] : v[j];
+    for (int j = 0; j < R; ++j, dst += p.ld_out)
+        if (j < rows) {
+            if (ADD) *dst += v[j];
+            else __stcs(dst, v[j]);
+        }
 }
 
 // n zeros from dst by `threads` threads, 16 bytes a store between the ends.
@@ -269,9 +308,9 @@ __device__ __forceinline__ void zero_run(T *dst, int64_t n, int thread, int thre
 // The same as bf16.  Neighbouring lanes exchange values: the even lane stores
 // row j, the odd lane row j + 1, both of columns m & ~1 and m | 1, so a store
 // instruction writes 2 rows x 64 bytes.
-template <bool ADD>
+template <bool ADD, int R>
 __device__ __forceinline__ void store_rows(const Params &p, __nv_bfloat16 *out, int64_t row, int rows, int64_t m,
-                                           const float (&v)[32])
+                                           const float (&v)[R])
 {
     const int odd = (int)(threadIdx.x & 1);
     const int64_t me = m - odd;
@@ -280,7 +319,7 @@ __device__ __forceinline__ void store_rows(const Params &p, __nv_bfloat16 *out, 
     const bool pair = p.pairs != 0 && has_hi;
     rows -= odd;
 #pragma unroll
-    for (int j = 0; j < 32; j += 2, dst += 2 * p.ld_out) {
+    for (int j = 0; j < R; j += 2, dst += 2 * p.ld_out) {
         const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
         float lo = odd ? got : v[j], hi = odd ? v[j + 1] : got;
         if (ADD) {
@@ -400,8 +439,8 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
             if (one) ptx::prefetch_tmap(tm);
             uint32_t stage = 0, phase = 0;
             bool ok = true;
-            for (int t = unit; ok && t < total; t += n_units) {
-                const Tile w = tile_at<MODE>(p, sh, t);
+            for (Walk<MODE> at(p, unit, n_units); ok && at.t < total; at.next(p, n_units)) {
+                const Tile w = tile_at<MODE>(p, sh, at);
                 // this CTA's half of the operand
                 const int half_n = w.nt / 2;
                 const int mn = (int)(m_side ? w.m0 + rank * 128 : w.n0 + (int)rank * half_n);
@@ -466,8 +505,8 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
             const uint64_t b_desc = B_MN ? ptx::make_sdesc(s0 + OPER_BYTES, BOX_BYTES, 1024, 2)
                                          : ptx::make_sdesc(s0 + OPER_BYTES, 16, 1024, 2);
             int iter = 0;                                // accumulators handed over
-            for (int t = unit; ok && t < total; t += n_units) {
-                const Tile w = tile_at<MODE>(p, sh, t);
+            for (Walk<MODE> at(p, unit, n_units); ok && at.t < total; at.next(p, n_units)) {
+                const Tile w = tile_at<MODE>(p, sh, at);
                 const uint32_t idesc = ptx::idesc_bf16(TILE, (uint32_t)w.nt) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
                 const int64_t len = MODE == WGRAD ? (int64_t)(w.r1 - w.r0) : p.red;
                 for (int kb = 0; kb < w.stages;) {
@@ -533,8 +572,8 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
         if (MODE == WGRAD) {
             // --------------------- zero the surplus rows of ragged stages
             uint32_t stage = 0, parity = 0;             // one parity bit per stage's raw barrier
-            for (int t = unit; t < total; t += n_units) {
-                const Tile w = tile_at<MODE>(p, sh, t);
+            for (Walk<MODE> at(p, unit, n_units); at.t < total; at.next(p, n_units)) {
+                const Tile w = tile_at<MODE>(p, sh, at);
                 if (w.stages == 0) continue;
                 const uint32_t s = (stage + (uint32_t)(w.stages - 1)) % STAGES;
                 stage = (s + 1) % STAGES;
@@ -562,45 +601,49 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
         const int q = warp & 3, half = (warp - EPI_WARP0) >> 2;
         const int m_in_tile = (int)rank * 128 + q * 32 + lane;
         int iter = 0;
-        for (int t = unit; t < total; t += n_units) {
-            const Tile w = tile_at<MODE>(p, sh, t);
+        for (Walk<MODE> at(p, unit, n_units); at.t < total; at.next(p, n_units)) {
+            const Tile w = tile_at<MODE>(p, sh, at);
             const int64_t m = w.m0 + m_in_tile;
-            if (MODE == WGRAD) {
-                if (w.stages == 0) {
-                    // an empty segment's gradient: its tiles share out the
-                    // expert's N x K zeros as one contiguous run
-                    if (!ADD) {
-                        const int64_t all = p.out_n * p.ld_out, per = (int64_t)p.m_tiles * p.n_tiles;
-                        const int64_t i = w.m0 / TILE * p.n_tiles + w.n0 / TILE;
-                        const int64_t share = ((all + per - 1) / per + 15) / 16 * 16;
-                        const int64_t lo = min(all, i * share), hi = min(all, lo + share);
-                        OutT *base = reinterpret_cast<OutT *>(p.out) + ((int64_t)w.split * p.E + w.e) * all;
-                        zero_run(base + lo, hi - lo, (int)rank * 32 * EPI_WARPS + (warp - EPI_WARP0) * 32 + lane,
-                                 2 * 32 * EPI_WARPS);
-                    }
-                    continue;
+            if (MODE == WGRAD && w.stages == 0) {
+                // an empty segment's gradient: its tiles share out the
+                // expert's N x K zeros as one contiguous run
+                if (!ADD) {
+                    const int64_t all = p.out_n * p.ld_out, per = (int64_t)p.m_tiles * p.n_tiles;
+                    const int64_t i = w.m0 / TILE * p.n_tiles + w.n0 / TILE;
+                    const int64_t share = ((all + per - 1) / per + 15) / 16 * 16;
+                    const int64_t lo = min(all, i * share), hi = min(all, lo + share);
+                    OutT *base = reinterpret_cast<OutT *>(p.out) + ((int64_t)w.split * p.E + w.e) * all;
+                    zero_run(base + lo, hi - lo, (int)rank * 32 * EPI_WARPS + (warp - EPI_WARP0) * 32 + lane,
+                             2 * 32 * EPI_WARPS);
                 }
-                // row n of the gradient = TMEM column, its column k = lane
-                const int64_t n = w.n0 + half * 128;
-                const int64_t row = ((int64_t)w.split * p.E + w.e) * p.out_n + n;
-                const int rows = (int)(w.n_end - n);
+                continue;
+            }
+            // lane = column m of the output, TMEM columns = its rows (WGRAD: rows n
+            // of the expert's gradient)
+            const int half_n = MODE == WGRAD ? TILE / 2 : w.nt / 2;
+            const int64_t n = w.n0 + half * half_n;
+            const int64_t row = MODE == WGRAD ? ((int64_t)w.split * p.E + w.e) * p.out_n + n : n;
+            const int rows = (int)(w.n_end - n);
+            const uint32_t src0 = tmem + (uint32_t)(half * half_n) + ((uint32_t)(q * 32) << 16);
+            OutT *out = reinterpret_cast<OutT *>(p.out);
+            if (MODE == WGRAD && w.chunk < w.stages) {
+                // several accumulators: summed in registers
                 float v[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) v[i] = 0.0f;
                 bool ok = true;
-                for (int kb = w.chunk; kb < w.stages; kb += w.chunk, ++iter) {       // all chunks but the last
+                for (int kb = 0; kb < w.stages; kb += w.chunk, ++iter) {
                     const int acc = iter & 1;
                     ok = wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p);
                     if (!ok) break;
                     ptx::tc_fence_after();
-                    const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)half * 128 + ((uint32_t)(q * 32) << 16);
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 128; c += 32) {
                         uint32_t x[32];
-                        ptx::tmem_ld_32x32b_x32(src + c * 32, x);
+                        ptx::tmem_ld_32x32b_x32(src0 + (uint32_t)(acc * TILE + c), x);
                         ptx::tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) v[c * 32 + i] += __uint_as_float(x[i]);
+                        for (int i = 0; i < 32; ++i) v[c + i] += __uint_as_float(x[i]);
                     }
                     // the accumulator is free once both CTAs' warps have read it
                     ptx::tc_fence_before();
@@ -608,57 +651,34 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
                 }
                 if (!ok) break;
-                const int acc = iter & 1;
-                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p))
-                    break;
-                ++iter;
-                ptx::tc_fence_after();
-                // the last chunk's columns are stored as they are read: the stores
-                // drain while the next columns come
-                const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)half * 128 + ((uint32_t)(q * 32) << 16);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    float y[32];
-                    uint32_t x[32];
-                    ptx::tmem_ld_32x32b_x32(src + c * 32, x);
-                    ptx::tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) y[i] = v[c * 32 + i] + __uint_as_float(x[i]);
-                    if (c == 3) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
-                    }
-                    store_rows<ADD>(p, reinterpret_cast<OutT *>(p.out), row + c * 32, rows - c * 32, m, y);
-                    __syncwarp();                        // lanes without an output rejoin before the collective load
-                }
-            } else {
-                const int acc = iter & 1;
-                if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p))
-                    break;
-                ++iter;
-                ptx::tc_fence_after();
-                const int half_n = w.nt / 2;
-                const uint32_t src = tmem + (uint32_t)acc * TILE + (uint32_t)(half * half_n) + ((uint32_t)(q * 32) << 16);
-                // lane = output column m, TMEM columns = output rows
+                store_rows<ADD>(p, out, row, rows, m, v);
+                __syncwarp();                            // lanes without an output rejoin before the collective load
+                continue;
+            }
+            const int acc = iter & 1;
+            if (!wait_bar(ptx::smem_u32(&sh->tmem_full[acc]), (uint32_t)((iter >> 1) & 1), abort_flag, p)) break;
+            ++iter;
+            ptx::tc_fence_after();
+            // 16 columns are stored while the next 16 come from TMEM
+            const uint32_t src = src0 + (uint32_t)(acc * TILE);
+            uint32_t x[COLS], y[COLS];
+            ptx::tmem_ld_32x32b_x16(src, x);
 #pragma unroll 1
-                for (int c = 0; c < half_n; c += 32) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32x32b_x32(src + c, v);
-                    ptx::tmem_ld_wait();
-                    if (c + 32 >= half_n) {
-                        ptx::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
-                    }
-                    const int64_t r = w.n0 + half * half_n + c;
-                    const int rows = (int)(w.n_end - r);
-                    float y[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) y[j] = __uint_as_float(v[j]);
-                    store_rows<false>(p, reinterpret_cast<OutT *>(p.out), r, rows, m, y);
-                    __syncwarp();                        // lanes without an output rejoin before the collective load
+            for (int c = 0; c < half_n; c += 2 * COLS) {
+                ptx::tmem_ld_wait(x);
+                ptx::tmem_ld_32x32b_x16(src + c + COLS, y);
+                store_rows<ADD>(p, out, row + c, rows - c, m, reinterpret_cast<const float (&)[COLS]>(x));
+                __syncwarp();                            // lanes without an output rejoin before the collective load
+                ptx::tmem_ld_wait(y);
+                if (c + 2 * COLS < half_n) ptx::tmem_ld_32x32b_x16(src + c + 2 * COLS, x);
+                else {
+                    // the accumulator is free once both CTAs' warps have read it
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster_relaxed(ptx::mapa_shared(ptx::smem_u32(&sh->tmem_empty[acc]), 0));
                 }
+                store_rows<ADD>(p, out, row + c + COLS, rows - c - COLS, m, reinterpret_cast<const float (&)[COLS]>(y));
+                __syncwarp();
             }
         }
     }
