@@ -71,6 +71,13 @@ int64_t integer(PyObject *o)
     return v;
 }
 
+bool truth(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw PythonError();
+    return v == 1;
+}
+
 ScalarType dtype(PyObject *o, const char *name)
 {
     const ScalarType t = THPDtype_Check(o) ? reinterpret_cast<THPDtype *>(o)->scalar_type : ScalarType::Undefined;
@@ -164,7 +171,7 @@ PyObject *ragged_gemm(PyObject *const *v)
 {
     const Tensor &a = tensor(v[0], "ragged_gemm: a"), &w = tensor(v[1], "ragged_gemm: w"),
                  &offsets = tensor(v[2], "ragged_gemm: offsets");
-    const bool transpose = PyObject_IsTrue(v[3]) == 1;
+    const bool transpose = truth(v[3]);
     const Call c(a);
     if (w.dim() != 3 || w.scalar_type() != BF16 || !w.is_contiguous())
         refuse("ragged_gemm: w must be contiguous bf16 [E, N, K]");
@@ -196,6 +203,7 @@ PyObject *ragged_wgrad(PyObject *const *v)
     const Call c(g);
     if (g.dim() != 2 || a.dim() != 2) refuse("ragged_wgrad: g and a must be [M, N] and [M, K]");
     const int64_t M = g.size(0), N = g.size(1), K = a.size(1), E = offsets.numel() - 1;
+    if (E < 1) refuse("ragged_wgrad: offsets: need Int with E + 1 elements, got " + shape_of(offsets));
     const int64_t ldg = c.matrix(g, "ragged_wgrad: g", BF16, M, N);
     const int32_t *off = c.vector<int32_t>(offsets, "ragged_wgrad: offsets", I32, E + 1);
     const bool kept = !none(v[2]);
@@ -211,7 +219,7 @@ PyObject *ragged_wgrad(PyObject *const *v)
     } else {
         lda = c.matrix(a, "ragged_wgrad: a", BF16, M, K);
     }
-    const bool accumulate = PyObject_IsTrue(v[7]) == 1;
+    const bool accumulate = truth(v[7]);
     ScalarType type = dtype(v[6], "ragged_wgrad: out_dtype");
     Tensor out;
     if (!none(v[5])) {
@@ -420,7 +428,9 @@ PyObject *nvfp4_gemv(PyObject *const *v)
                std::to_string(K / 2) + "], got " + shape_of(codes));
     c.same_device(codes, "nvfp4_gemv: codes");
     const int64_t need_scales = E * ((N + 127) / 128 * 128) * (K / 16);
-    if (scales.scalar_type() != U8 || !scales.is_contiguous() || scales.numel() < need_scales)
+    // one expert's scales follow another's: a longer buffer would be read at the wrong places
+    if (scales.scalar_type() != U8 || !scales.is_contiguous() || scales.numel() < need_scales ||
+        (E > 1 && scales.numel() != need_scales))
         refuse("nvfp4_gemv: scales must be contiguous uint8 with " + std::to_string(need_scales) + " bytes, got " +
                shape_of(scales));
     c.same_device(scales, "nvfp4_gemv: scales");

@@ -280,7 +280,7 @@ extern "C" nvfp4_status moe_route(const float *logits_dev, int64_t T, int32_t E,
                                   void *workspace, size_t workspace_bytes, void *stream)
 {
     cudaStream_t st = (cudaStream_t)stream;
-    NVFP4_REQUIRE(offsets_dev && row_token_dev && row_gate_dev &&
+    NVFP4_REQUIRE(offsets_dev && (M_pad_max == 0 || (row_token_dev && row_gate_dev)) &&
                   (T == 0 || (logits_dev && topk_idx_dev && topk_gate_dev && dst_row_dev)), NVFP4_ERR_INVALID_ARG,
                   "moe_route: null pointer");
     NVFP4_REQUIRE(T >= 0 && E >= 1 && E <= MAX_EXPERTS && k_r >= 1 && k_r <= MAX_TOPK && k_r <= E,
@@ -296,7 +296,7 @@ extern "C" nvfp4_status moe_route(const float *logits_dev, int64_t T, int32_t E,
                   "moe_route: workspace of %zu bytes required", need);
     int32_t *blkcnt = reinterpret_cast<int32_t *>(workspace);
     const int nblk = (int)((T + RB - 1) / RB);
-    if (cudaMemsetAsync(row_token_dev, 0xFF, (size_t)M_pad_max * 4, st) != cudaSuccess)
+    if (M_pad_max > 0 && cudaMemsetAsync(row_token_dev, 0xFF, (size_t)M_pad_max * 4, st) != cudaSuccess)
         return check_launch("moe_route memset");
     if (nblk > 0) {
         k_route_topk<<<(unsigned)nblk, 1024, 0, st>>>(logits_dev, T, E, k_r, topk_idx_dev, topk_gate_dev, blkcnt);

@@ -22,6 +22,7 @@ library's kernels plus one memset of Y.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import torch
@@ -33,6 +34,19 @@ def rac_channels(percent: float, K: int) -> int:
     """RAC channel count for "the top k% of channels" (gist.science/it 2.2 B,
     e.g. 50%): round(percent / 100 * K)."""
     return int(round(percent / 100.0 * K))
+
+
+def _same_device(what: str, weight: torch.Tensor, **tensors):
+    """The routing calls take bare pointers: every tensor has to be where the
+    layer's weights are."""
+    for name, t in tensors.items():
+        if t.device != weight.device:
+            raise ValueError(f"{what}: {name} is on {t.device}, the layer on {weight.device}")
+
+
+def _current(device):
+    """The device whose stream the calls go to, as the current one."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 class MoELayerW4A4:
@@ -162,13 +176,18 @@ class MoELayerW4A4:
         launches after the routing.  x bf16 [t, H], logits f32 [t, E]; returns
         f32 [t, H], a new tensor.  Bound by the weights of the experts in use;
         from a few dozen tokens on, forward's grouped GEMM is the faster form."""
+        _same_device("decode", self.c13, x=x, logits=logits)
+        if tuple(x.shape) != (logits.shape[0], self.H) or tuple(logits.shape) != (logits.shape[0], self.E):
+            raise ValueError(f"decode: need x [t, {self.H}] and logits [t, {self.E}], got {tuple(x.shape)} and "
+                             f"{tuple(logits.shape)}")
         if logits.shape[0] == 0:
             return torch.empty(0, self.H, dtype=torch.float32, device=x.device)
-        r = api.route(logits, self.k_r, seg_align=1)
-        h = api.nvfp4_gemv(x, self.c13, self.sf13, self.s13, 2 * self.I, self.H, expert_idx=r.topk_idx,
-                           epilogue=api.EPI_SWIGLU_BF16)
-        return api.nvfp4_gemv(h, self.c2, self.sf2, self.s2, self.H, self.I, expert_idx=r.topk_idx,
-                              epilogue=api.EPI_COMBINE_F32, gate=r.topk_gate)
+        with _current(x.device):
+            r = api.route(logits, self.k_r, seg_align=1)
+            h = api.nvfp4_gemv(x, self.c13, self.sf13, self.s13, 2 * self.I, self.H, expert_idx=r.topk_idx,
+                               epilogue=api.EPI_SWIGLU_BF16)
+            return api.nvfp4_gemv(h, self.c2, self.sf2, self.s2, self.H, self.I, expert_idx=r.topk_idx,
+                                  epilogue=api.EPI_COMBINE_F32, gate=r.topk_gate)
 
     def _route_into(self, logits):
         lib = api._lib.load()
@@ -274,15 +293,17 @@ class MoELayerW4A16:
         if tuple(x.shape) != (self.T, self.H) or tuple(logits.shape) != (self.T, self.E):
             raise ValueError(f"forward_train: need x [{self.T}, {self.H}] and logits [{self.T}, {self.E}], got "
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
+        _same_device("forward_train", self.wq13, x=x, logits=logits)
         if not hasattr(self, "x8"):
             self._train_buffers(x.device)
-        r = self.train_routing = api.route(logits, self.k_r, seg_align=1)
-        api.act8_quantize(x, out=self.x8)
-        api.routed_rows_bf16(x, r.row_token, r.m_pad_max, out=self.rows_h)
-        api.ragged_gemm(self.rows_h, self.wq13, r.offsets, out=self.y13)
-        api.swiglu_act8(self.y13, h=self.h_t, out=self.y8)
-        api.ragged_gemm(self.h_t, self.wq2, r.offsets, out=self.rows_y)
-        return api.combine_rows(self.rows_y, r.dst_row, gate=r.topk_gate)
+        with _current(x.device):
+            r = self.train_routing = api.route(logits, self.k_r, seg_align=1)
+            api.act8_quantize(x, out=self.x8)
+            api.routed_rows_bf16(x, r.row_token, r.m_pad_max, out=self.rows_h)
+            api.ragged_gemm(self.rows_h, self.wq13, r.offsets, out=self.y13)
+            api.swiglu_act8(self.y13, h=self.h_t, out=self.y8)
+            api.ragged_gemm(self.h_t, self.wq2, r.offsets, out=self.rows_y)
+            return api.combine_rows(self.rows_y, r.dst_row, gate=r.topk_gate)
 
     def backward(self, dy: torch.Tensor, *, dw13: torch.Tensor | None = None, dw2: torch.Tensor | None = None,
                  accumulate: bool = False) -> LayerGrads:
@@ -296,15 +317,17 @@ class MoELayerW4A16:
             raise ValueError(f"backward: dy must be bf16 [{self.T}, {self.H}]")
         if accumulate and (dw13 is None or dw2 is None):
             raise ValueError("backward: accumulate needs dw13 and dw2")
-        # routed dY; u = dY W2, the gradient of h before the router's weight
-        api.routed_rows_bf16(dy, r.row_token, r.m_pad_max, out=self.rows_h)
-        api.ragged_gemm(self.rows_h, self.wq2, r.offsets, transpose=True, out=self.h_t)
-        api.swiglu_act8_backward(self.y8, self.h_t, row_gate=r.row_gate, dy=self.y13, gh=self.gh, dgate=self.dgate)
-        dw2 = api.ragged_wgrad(self.rows_h, self.gh, r.offsets, out=dw2, accumulate=accumulate)
-        dw13 = api.ragged_wgrad(self.y13, self.x8, r.offsets, a_rows=r.row_token, out=dw13, accumulate=accumulate)
-        api.ragged_gemm(self.y13, self.wq13, r.offsets, transpose=True, out=self.rows_y)
-        dx = api.combine_rows(self.rows_y, r.dst_row)
-        dlogits = api.route_backward(r.topk_idx, r.topk_gate, r.dst_row, self.dgate, self.E)
+        _same_device("backward", self.wq13, dy=dy)
+        with _current(dy.device):
+            # routed dY; u = dY W2, the gradient of h before the router's weight
+            api.routed_rows_bf16(dy, r.row_token, r.m_pad_max, out=self.rows_h)
+            api.ragged_gemm(self.rows_h, self.wq2, r.offsets, transpose=True, out=self.h_t)
+            api.swiglu_act8_backward(self.y8, self.h_t, row_gate=r.row_gate, dy=self.y13, gh=self.gh, dgate=self.dgate)
+            dw2 = api.ragged_wgrad(self.rows_h, self.gh, r.offsets, out=dw2, accumulate=accumulate)
+            dw13 = api.ragged_wgrad(self.y13, self.x8, r.offsets, a_rows=r.row_token, out=dw13, accumulate=accumulate)
+            api.ragged_gemm(self.y13, self.wq13, r.offsets, transpose=True, out=self.rows_y)
+            dx = api.combine_rows(self.rows_y, r.dst_row)
+            dlogits = api.route_backward(r.topk_idx, r.topk_gate, r.dst_row, self.dgate, self.E)
         return LayerGrads(dx, dlogits, dw13, dw2)
 
     _route_into = MoELayerW4A4._route_into

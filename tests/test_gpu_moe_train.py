@@ -209,3 +209,43 @@ def test_dense_decode(cuda):
     y = lay.decode(x)
     wd = values(lay.c_w, lay.sf_w, lay.s_w, 256, 256)[0]
     assert rel_fro(y.cpu().numpy(), (x.double() @ wd.t()).cpu().numpy()) <= 1e-5
+
+
+def test_training_step_of_no_tokens(cuda):
+    lay, _, _ = layer(MoELayerW4A16, 0, 4, 64, 64, 2)
+    y = lay.forward_train(rnd(1, 0, 64), rnd(2, 0, 4, dtype=torch.float32))
+    g = lay.backward(rnd(3, 0, 64))
+    assert y.shape == g.dx.shape == (0, 64) and g.dlogits.shape == (0, 4)
+    assert not bool(g.dw13.any()) and not bool(g.dw2.any())
+
+
+def test_training_step_strided_and_two_layers_in_flight(cuda):
+    """x and dy on a longer row stride give the same bits; so do two layers
+    whose steps run on two streams at once."""
+    T, E, H, I, kr = 200, 8, 256, 128, 2
+    lays = [layer(MoELayerW4A16, T, E, H, I, kr, seed=s)[0] for s in (40, 50)]
+    xs, ls, dys = ([rnd(s + i, T, n, dtype=d) for i in range(2)] for s, n, d in
+                   ((60, H, BF16), (62, E, torch.float32), (64, H, BF16)))
+
+    def step(i, x, dy):
+        y = lays[i].forward_train(x, ls[i])
+        g = lays[i].backward(dy)
+        return y, g.dx, g.dlogits, g.dw13, g.dw2
+
+    want = [step(i, xs[i], dys[i]) for i in range(2)]
+    wide = [torch.full((T, H + 24), float("nan"), dtype=BF16, device=cuda) for _ in range(2)]
+    for w, t in zip(wide, (xs[0], dys[0])):
+        w[:, 8:8 + H] = t
+    for a, b in zip(step(0, wide[0][:, 8:8 + H], wide[1][:, 8:8 + H]), want[0]):
+        assert torch.equal(a, b)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(4):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(i, xs[i], dys[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            for a, b in zip(r, want[i]):
+                assert torch.equal(a, b)

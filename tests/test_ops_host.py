@@ -237,3 +237,52 @@ def test_missing_binding_fails_loudly(monkeypatch):
     monkeypatch.delattr(pkg, "_binding", raising=False)
     with pytest.raises(RuntimeError, match="not built"):
         _lib.binding()
+
+
+def test_binding_refuses_lengths_and_flags():
+    """Scale buffers with room between the experts, empty offset tables, flags
+    without a truth value."""
+    calls = good_calls()
+    u8, i32 = (lambda *n: torch.zeros(*n, dtype=torch.uint8)), (lambda *n: torch.zeros(*n, dtype=torch.int32))
+    with pytest.raises(ValueError, match="scales must be"):
+        calls["nvfp4_gemv"](scales=u8(3, 512 + 16))
+    for n in (0, 1):
+        with pytest.raises(ValueError, match="offsets: need"):
+            calls["ragged_wgrad"](offsets=i32(n))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        calls["ragged_gemm"](transpose=torch.ones(2))
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        calls["ragged_wgrad"](accumulate=torch.ones(2))
+
+
+def test_layers_refuse_tensors_elsewhere():
+    """The layers' calls pass bare pointers on: a tensor that is not where the
+    weights are is refused before any of them."""
+    from quantization_nvfp4_quantize_b200.moe import MoELayerW4A4, MoELayerW4A16
+    x, logits = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2, 4)
+    t = MoELayerW4A16.__new__(MoELayerW4A16)
+    t.T, t.H, t.E, t.k_r, t.I, t.train_routing = 2, 64, 4, 2, 32, object()
+    t.wq13 = torch.empty(4, 64, 64, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="forward_train: x is on cpu"):
+        t.forward_train(x, logits)
+    with pytest.raises(ValueError, match="forward_train: logits is on cpu"):
+        t.forward_train(x.to("meta"), logits)
+    with pytest.raises(ValueError, match="backward: dy is on cpu"):
+        t.backward(x)
+    d = MoELayerW4A4.__new__(MoELayerW4A4)
+    d.H, d.E, d.c13 = 64, 4, torch.empty(4, 64, 32, dtype=torch.uint8, device="meta")
+    with pytest.raises(ValueError, match="decode: x is on cpu"):
+        d.decode(x, logits)
+    d.c13 = torch.empty(4, 64, 32, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="decode: need x"):
+        d.decode(x[:, :32], logits)
+    with pytest.raises(ValueError, match="decode: need x"):
+        d.decode(x, logits[:1])
+
+
+def test_route_of_no_tokens_without_padding_needs_no_rows():
+    lib = _lib.load()
+    # rejected for its workspace only
+    assert lib.moe_route(None, 0, 8, 2, None, None, 1, FAKE, None, None, None, 0, None, 0, None) == WORKSPACE
+    assert lib.moe_route(None, 0, 8, 2, None, None, 1, None, None, None, None, 0, FAKE, 4096, None) == INVALID
+    assert lib.moe_route(None, 0, 8, 2, None, None, 1, FAKE, None, None, None, 8, FAKE, 4096, None) == INVALID
