@@ -173,7 +173,7 @@ class MoELayerW4A4:
         """The layer for the few tokens of a decode step (any number of rows,
         not the constructor's): the same NVFP4 weights, activations in BF16
         (W4A16: nothing is quantized or compensated), two matrix-vector
-        launches after the routing.  x bf16 [t, H], logits f32 [t, E]; returns
+        calls after the routing.  x bf16 [t, H], logits f32 [t, E]; returns
         f32 [t, H], a new tensor.  Bound by the weights of the experts in use;
         from a few dozen tokens on, forward's grouped GEMM is the faster form."""
         _same_device("decode", self.c13, x=x, logits=logits)
