@@ -251,7 +251,9 @@ class MoELayerW4A16:
 
     def set_weights(self, w13: torch.Tensor, w2: torch.Tensor):
         """Fake-quantize new bf16 weights into the layer (the per-step work of
-        QAT, where the weights change every optimizer step)."""
+        QAT, where the weights change every optimizer step).  What forward_train
+        kept belongs to the old ones: backward refuses until its next call."""
+        self.train_routing = None
         lib = api._lib.load()
         st = api._stream(w13.device)
         for w, wq, s_t in ((w13, self.wq13, self.s13), (w2, self.wq2, self.s2)):
@@ -289,28 +291,35 @@ class MoELayerW4A16:
     def forward_train(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """The layer with what backward needs kept in 8 bits: X (per token, not
         per routed copy) and the gate/up rows.  Returns Y f32 [T, H], a new
-        tensor.  I must be a multiple of 32."""
+        tensor.  I must be a multiple of 32.  After a call that fails on its way
+        nothing is kept."""
         if tuple(x.shape) != (self.T, self.H) or tuple(logits.shape) != (self.T, self.E):
             raise ValueError(f"forward_train: need x [{self.T}, {self.H}] and logits [{self.T}, {self.E}], got "
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
+        if x.dtype != torch.bfloat16 or logits.dtype != torch.float32:
+            raise ValueError(f"forward_train: x must be bf16 and logits f32, got {x.dtype} and {logits.dtype}")
         _same_device("forward_train", self.wq13, x=x, logits=logits)
         if not hasattr(self, "x8"):
             self._train_buffers(x.device)
+        self.train_routing = None
         with _current(x.device):
-            r = self.train_routing = api.route(logits, self.k_r, seg_align=1)
+            r = api.route(logits, self.k_r, seg_align=1)
             api.act8_quantize(x, out=self.x8)
             api.routed_rows_bf16(x, r.row_token, r.m_pad_max, out=self.rows_h)
             api.ragged_gemm(self.rows_h, self.wq13, r.offsets, out=self.y13)
             api.swiglu_act8(self.y13, h=self.h_t, out=self.y8)
             api.ragged_gemm(self.h_t, self.wq2, r.offsets, out=self.rows_y)
-            return api.combine_rows(self.rows_y, r.dst_row, gate=r.topk_gate)
+            y = api.combine_rows(self.rows_y, r.dst_row, gate=r.topk_gate)
+        self.train_routing = r
+        return y
 
     def backward(self, dy: torch.Tensor, *, dw13: torch.Tensor | None = None, dw2: torch.Tensor | None = None,
                  accumulate: bool = False) -> LayerGrads:
         """Gradients of the last forward_train for dY (bf16 [T, H]), with its
         weights (call it before set_weights).  dw13 / dw2: where the weight
-        gradients go (f32 or bf16); accumulate adds to them."""
-        r = getattr(self, "train_routing", None)
+        gradients go (f32 or bf16, contiguous); accumulate adds to them.  A
+        refused call changes neither."""
+        r = self.train_routing
         if r is None:
             raise RuntimeError("backward: no forward_train to differentiate")
         if tuple(dy.shape) != (self.T, self.H) or dy.dtype != torch.bfloat16:
@@ -318,6 +327,14 @@ class MoELayerW4A16:
         if accumulate and (dw13 is None or dw2 is None):
             raise ValueError("backward: accumulate needs dw13 and dw2")
         _same_device("backward", self.wq13, dy=dy)
+        if dy.stride(1) != 1 and self.H > 1:
+            raise ValueError("backward: dy: columns must be contiguous")
+        for name, d, w in (("dw13", dw13, self.wq13), ("dw2", dw2, self.wq2)):
+            if d is None:
+                continue
+            _same_device("backward", self.wq13, **{name: d})
+            if d.shape != w.shape or d.dtype not in (torch.float32, torch.bfloat16) or not d.is_contiguous():
+                raise ValueError(f"backward: {name} must be contiguous f32 or bf16 {list(w.shape)}")
         with _current(dy.device):
             # routed dY; u = dY W2, the gradient of h before the router's weight
             api.routed_rows_bf16(dy, r.row_token, r.m_pad_max, out=self.rows_h)

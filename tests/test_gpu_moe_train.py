@@ -249,3 +249,30 @@ def test_training_step_strided_and_two_layers_in_flight(cuda):
         for r in got[i]:
             for a, b in zip(r, want[i]):
                 assert torch.equal(a, b)
+
+
+def test_nothing_kept_after_a_failed_forward_or_new_weights(cuda, monkeypatch):
+    """backward never mixes a forward's routing with another's rows or weights."""
+    lay, w13, w2 = layer(MoELayerW4A16, 8, 4, 64, 64, 2)
+    x, logits, dy = rnd(1, 8, 64), rnd(2, 8, 4, dtype=torch.float32), rnd(3, 8, 64)
+    lay.forward_train(x, logits)
+    want = lay.backward(dy)
+    with pytest.raises(ValueError, match="x must be bf16"):
+        lay.forward_train(x.float(), logits)
+    assert torch.equal(lay.backward(dy).dx, want.dx)
+
+    def fail(*args, **kw):
+        raise MemoryError
+
+    from quantization_nvfp4_quantize_b200 import api
+    with monkeypatch.context() as m:
+        m.setattr(api, "combine_rows", fail)
+        with pytest.raises(MemoryError):
+            lay.forward_train(rnd(4, 8, 64), logits)
+    with pytest.raises(RuntimeError, match="no forward_train"):
+        lay.backward(dy)
+    lay.forward_train(x, logits)
+    assert torch.equal(lay.backward(dy).dx, want.dx)
+    lay.set_weights(w13, w2)
+    with pytest.raises(RuntimeError, match="no forward_train"):
+        lay.backward(dy)

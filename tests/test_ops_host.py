@@ -286,3 +286,25 @@ def test_route_of_no_tokens_without_padding_needs_no_rows():
     assert lib.moe_route(None, 0, 8, 2, None, None, 1, FAKE, None, None, None, 0, None, 0, None) == WORKSPACE
     assert lib.moe_route(None, 0, 8, 2, None, None, 1, None, None, None, None, 0, FAKE, 4096, None) == INVALID
     assert lib.moe_route(None, 0, 8, 2, None, None, 1, FAKE, None, None, None, 8, FAKE, 4096, None) == INVALID
+
+
+def test_backward_refuses_destinations_before_any_call():
+    from quantization_nvfp4_quantize_b200.moe import MoELayerW4A16
+    t = MoELayerW4A16.__new__(MoELayerW4A16)
+    t.T, t.H, t.E, t.k_r, t.I, t.train_routing = 2, 64, 4, 2, 32, object()
+    t.wq13 = torch.empty(4, 64, 64, dtype=torch.bfloat16, device="meta")
+    t.wq2 = torch.empty(4, 64, 32, dtype=torch.bfloat16, device="meta")
+    dy = torch.empty(2, 64, dtype=torch.bfloat16, device="meta")
+    good = torch.empty(4, 64, 32, device="meta")
+    for bad, match in ((torch.empty(4, 64, 63, device="meta"), "dw13 must be"),
+                       (torch.empty(4, 64, 64, device="meta", dtype=torch.float16), "dw13 must be"),
+                       (torch.empty(4, 64, 64, device="meta").transpose(1, 2), "dw13 must be"),
+                       (torch.empty(4, 64, 64), "dw13 is on cpu")):
+        with pytest.raises(ValueError, match=match):
+            t.backward(dy, dw13=bad, dw2=good, accumulate=True)
+    with pytest.raises(ValueError, match="columns must be contiguous"):
+        t.backward(torch.empty(64, 2, dtype=torch.bfloat16, device="meta").t())
+    x, logits = torch.empty(2, 64, device="meta"), torch.empty(2, 4, device="meta")
+    with pytest.raises(ValueError, match="x must be bf16"):
+        t.forward_train(x, logits)
+    assert t.train_routing is not None          # a refused call leaves what was kept
