@@ -20,7 +20,10 @@
 // mantissa bits, which reads as e2m1 * 2^-126 (its subnormal included); one
 // BF16 multiplication by sf * 2^117 gives e2m1 * sf * 2^-9, exact (at most 6
 // significant bits).  2^9 joins the tensor scale at the end.  The only
-// roundings of a product are those of the f32 accumulation.
+// roundings of a product are those of the f32 accumulation: the tensor core
+// truncates its additions, so a chunk's 8 MMAs start from zero and the chunks
+// are added in f32 (16 tokens, down 4096 x 1536: error 4.4e-7 -> 1.0e-7 in
+// norm, that of plain f32 sums, for 0.2% of the time).
 //
 // A warp takes 16 weight rows and 128 columns a step: lane (g, t) = (lane / 4,
 // lane % 4) loads 32 consecutive weights (16 bytes, two scale blocks) of row g
@@ -261,7 +264,10 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
         for (int k = 0; k < SETS; ++k) {
             const uint4 c[2] = {slot.c[2 * k][lane], slot.c[2 * k + 1][lane]};
             const uint32_t s[2] = {slot.s[lane][2 * k], slot.s[lane][2 * k + 1]};
-            compute_chunk(c, s, 2 * (t & 1), xp, acc[k]);
+            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            compute_chunk(c, s, 2 * (t & 1), xp, d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[k][j] += d[j];
         }
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");          // nothing in flight when the ring is reused
