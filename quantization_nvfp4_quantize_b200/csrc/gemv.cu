@@ -69,6 +69,7 @@ struct Params {
     const float *gate;
     void *out;
     int64_t ld_out;
+    int x_wide;                          // rows of x start on 32 bytes
 };
 
 __device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b)
@@ -111,33 +112,30 @@ __device__ __forceinline__ int tile_row(int tile, int rr)
     return (tile >> 3) * 128 + 32 * (g & 3) + 4 * (tile & 7) + (g >> 2) + 2 * (rr >> 3);
 }
 
-// A lane's pointers into one 16-row set: codes and scale words of row g, column
-// 0; row g + 8 (two weight rows further) lies c2 / s2 bytes on.  A row past
-// the end reads an existing one; its sums are not stored.
+// A lane's pointer into one 16-row set: codes of row g, column 0; row g + 8
+// (two weight rows further) lies c2 bytes on.  A row past the end reads an
+// existing one; its sums are not stored.
 struct Set {
     const uint8_t *c;
-    const uint8_t *s;
-    int32_t c2, s2;
+    int32_t c2;
 };
 
-__device__ __forceinline__ uint64_t scale_at(uint32_t n, uint32_t K)
-{
-    return (uint64_t)(n >> 7) * (K * 8u) + (n & 31u) * 16u + ((n >> 5) & 3u) * 4u;
-}
-
-__device__ __forceinline__ Set set_of(const Params &p, const uint8_t *codes, const uint8_t *scales, int tile, int row_base,
-                                      int rows)
+__device__ __forceinline__ Set set_of(const Params &p, const uint8_t *codes, int tile, int row_base, int rows)
 {
     const int r = tile_row(tile, (threadIdx.x & 31) >> 2);
-    const uint32_t n = (uint32_t)(row_base + min(r, rows - 1));
     Set l;
-    l.c = codes + (uint64_t)n * (uint32_t)(p.K >> 1);
-    l.s = scales + scale_at(n, (uint32_t)p.K);
-    const bool second = r + 2 < rows;
-    l.c2 = second ? p.K : 0;
-    // rows n and n + 2 share a 32-row quarter unless the set straddles one (SwiGLU's up rows)
-    l.s2 = second ? (int32_t)(scale_at(n + 2, (uint32_t)p.K) - scale_at(n, (uint32_t)p.K)) : 0;
+    l.c = codes + (uint64_t)(uint32_t)(row_base + min(r, rows - 1)) * (uint32_t)(p.K >> 1);
+    l.c2 = r + 2 < rows ? p.K : 0;
     return l;
+}
+
+// Scale word of a set's row rr, columns 0..63 (a row past the end: an existing
+// one's).
+__device__ __forceinline__ const uint8_t *scales_of(const Params &p, const uint8_t *scales, int tile, int row_base, int rows,
+                                                    int rr)
+{
+    const uint32_t n = (uint32_t)(row_base + min(tile_row(tile, rr), rows - 1));
+    return scales + (uint64_t)(n >> 7) * ((uint32_t)p.K * 8u) + (n & 31u) * 16u + ((n >> 5) & 3u) * 4u;
 }
 
 // 128 columns of one set: codes c and scale words s of its two rows, the
@@ -165,12 +163,31 @@ __device__ __forceinline__ void compute_chunk(const uint4 (&c)[2], const uint32_
     }
 }
 
-// One chunk's operands of a lane, in flight through shared memory: every lane
-// reads back only what it copied, so a group wait is all the synchronization.
+// One chunk's operands in flight through shared memory.  A lane reads back the
+// codes that it copied itself; the scale words are shared: the warp copies each
+// of its rows' two words (64 columns each) once, in an order that puts a lane's
+// rows side by side (set k, row g + 8 hi at g * 2 SETS + 2 k + hi).  Each lane
+// copying its own (four 4-byte copies a chunk instead of two, half of them
+// twice) took 11 us of the 75 that the loads of 16 tokens' down products take
+// by themselves.
 template <int SETS>
 struct Slot {
     uint4 c[2 * SETS][32];               // codes of the lane's rows
-    uint32_t s[32][2 * SETS];            // their scale words (64 columns)
+    uint32_t s[2][16 * (2 * SETS - 1)];  // scale words per 64 columns (the halves 16 banks apart)
+};
+
+// The lane's (half, row) among the scale words of its warp's copy j < SETS.
+template <int SETS>
+struct ScaleWord {
+    int half, pos, k, rr;
+    __device__ __forceinline__ ScaleWord(int j, int lane)
+    {
+        const int i = j * 32 + lane;
+        half = i / (16 * SETS);
+        pos = i % (16 * SETS);
+        k = pos / 2 % SETS;
+        rr = pos / (2 * SETS) + 8 * (pos & 1);
+    }
 };
 
 __device__ __forceinline__ void copy16(void *dst, const void *src)
@@ -183,26 +200,37 @@ __device__ __forceinline__ void copy4(void *dst, const void *src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
+// 32 bytes of x (32-byte aligned).
+__device__ __forceinline__ void load32(const __nv_bfloat16 *src, uint4 &a, uint4 &b)
+{
+    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+                 : "l"(src));
+}
+
 // Chunks of 128 columns ch0, ch0 + stride, ... below `chunks`, of SETS row sets
 // against the same x; DEPTH - 1 chunks are in flight while one is computed.
-// x: the lane's token row (a column without a token may take any row: its sums
-// are not stored).  K is a multiple of 64, so half of the last chunk may be
-// missing: its lanes read earlier columns again, against zeros of x.
+// s: this lane's rows for ScaleWord j.  x: the lane's token row (a column
+// without a token may take any row: its sums are not stored).  K is a multiple
+// of 64, so half of the last chunk may be missing: its lanes read earlier
+// columns again, against zeros of x.
 template <int SETS>
-__device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS], const __nv_bfloat16 *x, int ch0,
-                                          int stride, int chunks, int K, float (&acc)[SETS][4])
+__device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS], const uint8_t *const (&s)[SETS],
+                                          const __nv_bfloat16 *x, bool x_wide, int ch0, int stride, int chunks, int K,
+                                          float (&acc)[SETS][4])
 {
     const int lane = threadIdx.x & 31, t = lane & 3;
     if (ch0 >= chunks) return;
     const int n = (chunks - 1 - ch0) / stride + 1;
     const int step = stride * 128;
-    int col = ch0 * 128 + 32 * t;                                 // of the next chunk to copy
-    const int at = col < K ? col : col - 64;
+    int base = ch0 * 128;                                         // of the next chunk to copy
+    const int col0 = base + 32 * t;
+    const int at = col0 < K ? col0 : col0 - 64;
     const uint8_t *pc[SETS], *ps[SETS];
 #pragma unroll
     for (int k = 0; k < SETS; ++k) {
         pc[k] = l[k].c + (at >> 1);
-        ps[k] = l[k].s + (uint64_t)(at >> 6) * 512;
+        ps[k] = s[k] + (uint64_t)((base >> 6) + ScaleWord<SETS>(k, lane).half) * 512;
     }
     int issued = 0;
     auto issue = [&]() {
@@ -212,17 +240,15 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
             for (int k = 0; k < SETS; ++k) {
                 copy16(&slot.c[2 * k][lane], pc[k]);
                 copy16(&slot.c[2 * k + 1][lane], pc[k] + l[k].c2);
-                copy4(&slot.s[lane][2 * k], ps[k]);
-                copy4(&slot.s[lane][2 * k + 1], ps[k] + l[k].s2);
+                const ScaleWord<SETS> w(k, lane);
+                copy4(&slot.s[w.half][w.pos], base + 64 * w.half < K ? ps[k] : ps[k] - 512);
             }
             ++issued;
-            col += step;
-            if (col < K) {
+            base += step;
 #pragma unroll
-                for (int k = 0; k < SETS; ++k) {
-                    pc[k] += step / 2;
-                    ps[k] += step * 8;
-                }
+            for (int k = 0; k < SETS; ++k) {
+                if (base + 32 * t < K) pc[k] += step / 2;
+                ps[k] += step * 8;
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -230,14 +256,21 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
     uint4 v[4];
     const __nv_bfloat16 *px = x + at;
     auto load_x = [&]() {
+        if (x_wide) {
+            load32(px, v[0], v[1]);
+            load32(px + 16, v[2], v[3]);
+        } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(px) + k);
+            for (int k = 0; k < 4; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(px) + k);
+        }
     };
 #pragma unroll
     for (int i = 0; i < DEPTH - 1; ++i) issue();
     load_x();
-    int xcol = ch0 * 128 + 32 * t;                                // of the chunk whose x is in v
+    int xcol = col0;                                              // of the chunk whose x is in v
     for (int i = 0; i < n; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 2) : "memory");
+        __syncwarp();                                             // chunk i has landed, chunk i - 1 has been read, by every lane
         issue();
         uint32_t xp[16];
 #pragma unroll
@@ -258,19 +291,28 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
             if (xcol < K) px += step;
             load_x();
         }
-        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
         const Slot<SETS> &slot = ring[i % DEPTH];
+        const uint32_t *words = &slot.s[t >> 1][(lane >> 2) * 2 * SETS];
+        uint32_t w[2 * SETS];
+        if (SETS == 2) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(words);
+            w[0] = q.x; w[1] = q.y; w[2 * SETS - 2] = q.z; w[2 * SETS - 1] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2 *>(words);
+            w[0] = q.x; w[1] = q.y;
+        }
 #pragma unroll
         for (int k = 0; k < SETS; ++k) {
             const uint4 c[2] = {slot.c[2 * k][lane], slot.c[2 * k + 1][lane]};
-            const uint32_t s[2] = {slot.s[lane][2 * k], slot.s[lane][2 * k + 1]};
+            const uint32_t sw[2] = {w[2 * k], w[2 * k + 1]};
             float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            compute_chunk(c, s, 2 * (t & 1), xp, d);
+            compute_chunk(c, sw, 2 * (t & 1), xp, d);
 #pragma unroll
             for (int j = 0; j < 4; ++j) acc[k][j] += d[j];
         }
     }
-    asm volatile("cp.async.wait_group 0;" ::: "memory");          // nothing in flight when the ring is reused
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncwarp();                                                 // nothing in flight or unread when the ring is reused
 }
 
 __device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + expf(-z)); }
@@ -354,9 +396,13 @@ __global__ void __launch_bounds__(THREADS, BLOCKS) k_nvfp4_gemv(const Params p, 
         if (e >= 0) {
             const int pair = pair_of(min(m0 + g, members - 1));
             const uint8_t *codes = p.codes + e * p.code_stride, *scales = p.scales + e * p.scale_stride;
-            const Set l[2] = {set_of(p, codes, scales, tile0, 0, n_rows),
-                              set_of(p, codes, scales, tile1, FORM == SWIGLU ? n_rows : 0, n_rows)};
-            dot_range<2>(ring, l, p.x + (int64_t)((uint32_t)pair * p.x_mul >> 16) * p.ldx, split, splits, chunks, p.K, acc);
+            const int base1 = FORM == SWIGLU ? n_rows : 0;
+            const Set l[2] = {set_of(p, codes, tile0, 0, n_rows), set_of(p, codes, tile1, base1, n_rows)};
+            const ScaleWord<2> w(0, lane);                       // the same row for both halves
+            const uint8_t *row = scales_of(p, scales, w.k ? tile1 : tile0, w.k ? base1 : 0, n_rows, w.rr);
+            const uint8_t *const s[2] = {row, row};
+            dot_range<2>(ring, l, s, p.x + (int64_t)((uint32_t)pair * p.x_mul >> 16) * p.ldx, p.x_wide, split, splits, chunks,
+                         p.K, acc);
             coef = 512.0f * p.s_t[e];                            // the operands carry 2^-9
         }
         if (m0 > 0) __syncthreads();                             // the last pass's sums have been read
@@ -418,9 +464,10 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
         const int64_t pair = (int64_t)blockIdx.x * p.k_r + j;
         const int e = dense ? 0 : p.idx[pair];
         if (e >= 0 && e < p.E) {
-            const Set l[1] = {set_of(p, p.codes + e * p.code_stride, p.scales + e * p.scale_stride, tile, 0, p.N)};
+            const Set l[1] = {set_of(p, p.codes + e * p.code_stride, tile, 0, p.N)};
+            const uint8_t *const s[1] = {scales_of(p, p.scales + e * p.scale_stride, tile, 0, p.N, ScaleWord<1>(0, lane).rr)};
             float acc[1][4] = {{0, 0, 0, 0}};
-            dot_range<1>(ring, l, p.x + pair * p.ldx, ch, 1, ch_end, p.K, acc);
+            dot_range<1>(ring, l, s, p.x + pair * p.ldx, p.x_wide, ch, 1, ch_end, p.K, acc);
             const float coef = 512.0f * (p.gate ? p.gate[pair] * p.s_t[e] : p.s_t[e]);
             tot[0] += coef * acc[0][0];                          // column 0 is lane t = 0's
             tot[1] += coef * acc[0][2];
@@ -559,6 +606,7 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
                     ? (void *)(reinterpret_cast<__nv_bfloat16 *>(out_dev) + t0 * k_r * ld_out)
                     : (void *)(reinterpret_cast<float *>(out_dev) + (combine ? t0 : t0 * k_r) * ld_out);
         p.ld_out = ld_out;
+        p.x_wide = reinterpret_cast<uintptr_t>(p.x) % 32 == 0 && ldx % 16 == 0;
         const int64_t units = dense ? (tn + COLS - 1) / COLS : tn * k_r;
         const int64_t row_pairs = epilogue == MOE_EPI_SWIGLU_BF16 ? tiles : tiles / 2;
         const int splits = column_splits(units, row_pairs, K);
