@@ -4,11 +4,13 @@
 //   y[r, n] = s_t[e] * sum_k e2m1(w_e[n,k]) sf_e[n, k/16] x[r, k]
 //
 // The floor is HBM (0.5625 bytes per weight, each read once: 41 weights per
-// clock and SM); what bounds it is the decode.  A weight costs 3.9
-// thread-instructions in all (1.0 mask, 0.9 shift, 0.6 scale, 0.13 MMA, the rest
-// copies, x and addresses), the ALU pipe's share of them half of its time at the
-// HBM rate and the whole issue 1.2 times it: 82 experts of 4096 x 1536 (16
-// tokens, top-8 of 128) take 104 us against 45 for the bytes.
+// clock and SM); what bounds it is the decode, with the loads behind it.  A weight costs 3.7
+// thread-instructions in all (1.0 mask, 0.6 multiplication, 0.1 shift, 0.6 scale,
+// 0.13 MMA, the rest copies, x and addresses), the whole issue 1.2 times the HBM
+// rate: 82 experts of 4096 x 1536 (16 tokens, top-8 of 128) take 95 us against
+// 45 for the bytes.  (The copies and x without the products: 75 us; the products
+// with half the decode: 86.  Neither alone is the bound, and the registers allow
+// no more warps to overlap them.)
 // The multiply-adds go to mma.sync (m16n8k16, BF16, f32 accumulation), 16
 // weight rows times up to 8 tokens per instruction: the tensor pipe is idle
 // otherwise (13% with them), and a second token costs no decode.  Measured
@@ -101,7 +103,7 @@ __device__ __forceinline__ void decode8(uint32_t w, uint32_t p[4])
 __device__ __forceinline__ void mma16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1)
 {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -141,28 +143,34 @@ __device__ __forceinline__ const uint8_t *scales_of(const Params &p, const uint8
     return scales + (uint64_t)(n >> 7) * ((uint32_t)p.K * 8u) + (n & 31u) * 16u + ((n >> 5) & 3u) * 4u;
 }
 
-// 128 columns of one set: codes c and scale words s of its two rows, the
-// lane's two scale bytes being byte0 and byte0 + 1 of its word; the lane's 32 x
-// as pairs (i, i + 4) in xp.
-__device__ __forceinline__ void compute_chunk(const uint4 (&c)[2], const uint32_t (&s)[2], uint32_t byte0,
-                                              const uint32_t (&xp)[16], float (&acc)[4])
+// 128 columns of SETS row sets: codes c and scale words s of their rows (set
+// k: 2k, 2k + 1), the lane's two scale bytes being byte0 and byte0 + 1 of a
+// word; the lane's 32 x as pairs (i, i + 4) in xp.  The sets take turns, so one's
+// decode runs under the other's dependent MMAs (one token gate/up 9.55 ->
+// 9.27 us).
+template <int SETS>
+__device__ __forceinline__ void compute_chunk(const uint32_t (&c)[2 * SETS][4], const uint32_t (&s)[2 * SETS],
+                                              uint32_t byte0, const uint32_t (&xp)[16], float (&acc)[SETS][4])
 {
-    const uint32_t ca[4] = {c[0].x, c[0].y, c[0].z, c[0].w};
-    const uint32_t cb[4] = {c[1].x, c[1].y, c[1].z, c[1].w};
 #pragma unroll
     for (int blk = 0; blk < 2; ++blk) {
         const uint32_t pick = 0x4440u + byte0 + blk;
-        const uint32_t sa = scale_operand(__byte_perm(s[0], 0u, pick));
-        const uint32_t sb = scale_operand(__byte_perm(s[1], 0u, pick));
+        uint32_t sf[2 * SETS];
 #pragma unroll
-        for (int q = 2 * blk; q < 2 * blk + 2; ++q) {
-            uint32_t pa[4], pb[4];
-            decode8(ca[q], pa);
-            decode8(cb[q], pb);
-            mma16816(acc, bmul2(pa[0], sa), bmul2(pb[0], sb), bmul2(pa[1], sa), bmul2(pb[1], sb), xp[4 * q], xp[4 * q + 1]);
-            mma16816(acc, bmul2(pa[2], sa), bmul2(pb[2], sb), bmul2(pa[3], sa), bmul2(pb[3], sb), xp[4 * q + 2],
-                     xp[4 * q + 3]);
-        }
+        for (int r = 0; r < 2 * SETS; ++r) sf[r] = scale_operand(__byte_perm(s[r], 0u, pick));
+#pragma unroll
+        for (int q = 2 * blk; q < 2 * blk + 2; ++q)
+#pragma unroll
+            for (int k = 0; k < SETS; ++k) {
+                uint32_t pa[4], pb[4];
+                const uint32_t sa = sf[2 * k], sb = sf[2 * k + 1];
+                decode8(c[2 * k][q], pa);
+                decode8(c[2 * k + 1][q], pb);
+                mma16816(acc[k], bmul2(pa[0], sa), bmul2(pb[0], sb), bmul2(pa[1], sa), bmul2(pb[1], sb), xp[4 * q],
+                         xp[4 * q + 1]);
+                mma16816(acc[k], bmul2(pa[2], sa), bmul2(pb[2], sb), bmul2(pa[3], sa), bmul2(pb[3], sb), xp[4 * q + 2],
+                         xp[4 * q + 3]);
+            }
     }
 }
 
@@ -304,15 +312,18 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
             const uint2 q = *reinterpret_cast<const uint2 *>(words);
             w[0] = q.x; w[1] = q.y;
         }
+        uint32_t c[2 * SETS][4];
 #pragma unroll
-        for (int k = 0; k < SETS; ++k) {
-            const uint4 c[2] = {slot.c[2 * k][lane], slot.c[2 * k + 1][lane]};
-            const uint32_t sw[2] = {w[2 * k], w[2 * k + 1]};
-            float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            compute_chunk(c, sw, 2 * (t & 1), xp, d);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[k][j] += d[j];
+        for (int r = 0; r < 2 * SETS; ++r) {
+            const uint4 q = slot.c[r][lane];
+            c[r][0] = q.x; c[r][1] = q.y; c[r][2] = q.z; c[r][3] = q.w;
         }
+        float d[SETS][4] = {};
+        compute_chunk<SETS>(c, w, 2 * (t & 1), xp, d);
+#pragma unroll
+        for (int k = 0; k < SETS; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[k][j] += d[k][j];
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncwarp();                                                 // nothing in flight or unread when the ring is reused

@@ -166,3 +166,35 @@ def test_strides_and_surroundings(cuda):
     api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, out=buf[:, 2:2 + N])
     assert torch.equal(buf[:, 2:2 + N], api.nvfp4_gemv(x.contiguous(), codes, sf, s, N, K, expert_idx=idx))
     assert bool((buf[:, :2] == 4).all()) and bool((buf[:, 2 + N:] == 4).all())
+
+
+@pytest.mark.parametrize("K", [64, 192, 704, 1024])
+def test_rows_on_16_and_32_bytes(cuda, K):
+    """Rows of x that start on 16 bytes only are loaded in smaller pieces: the
+    same bits."""
+    E, N, T, kr = 6, 160, 11, 3
+    codes, sf, s, w = weights(20, E, N, K)
+    idx = torch.randint(0, E, (T, kr), dtype=I32, device=cuda)
+    gate = torch.rand(T, kr, device=cuda)
+    for form, rows, g in ((api.EPI_STORE_F32, T, None), (api.EPI_SWIGLU_BF16, T, None),
+                          (api.EPI_COMBINE_F32, T * kr, gate), (api.EPI_COMBINE_F32, kr, gate[:1])):
+        i = idx[:g.shape[0]] if g is not None else idx
+        x = rnd(21, rows, 2 * K)[:, :K].contiguous()
+        wide = torch.full((rows, K + 24), float("nan"), dtype=x.dtype, device=cuda)
+        wide[:, 8:8 + K] = x
+        a = api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=i, epilogue=form, gate=g)
+        assert torch.equal(a, api.nvfp4_gemv(wide[:, 8:8 + K], codes, sf, s, N, K, expert_idx=i, epilogue=form, gate=g))
+
+
+def test_long_sums(cuda):
+    """Sums of 8192 terms of one sign.  A chunk of 128 columns is 8 MMAs of 16
+    exact products and the sum so far: 17 terms cut to the largest's 24 bits,
+    8 * 17 * 2^-24 in all; 64 chunks and 4 warps are added in f32 (2^-24 each),
+    and the scale of the sum is rounded twice."""
+    N, K = 32, 8192
+    codes, sf, s, w = weights(22, 1, N, K)
+    codes = codes & 0x77
+    x = rnd(23, 3, 2 * K)[:, :K].abs().contiguous()
+    got = api.nvfp4_gemv(x, codes, sf, s, N, K)
+    want = x.double() @ w.abs()[0].t()
+    assert float(((got.double() - want).abs() / want).max()) <= (8 * 17 + 64 + 4 + 2) * 2.0 ** -24
