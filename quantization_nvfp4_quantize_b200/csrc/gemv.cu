@@ -4,18 +4,20 @@
 //   y[r, n] = s_t[e] * sum_k e2m1(w_e[n,k]) sf_e[n, k/16] x[r, k]
 //
 // The floor is HBM (0.5625 bytes per weight, each read once: 41 weights per
-// clock and SM); what bounds it is the decode, with the loads behind it.  A weight costs 3.7
-// thread-instructions in all (1.0 mask, 0.6 multiplication, 0.1 shift, 0.6 scale,
-// 0.13 MMA, the rest copies, x and addresses), the whole issue 1.2 times the HBM
-// rate: 82 experts of 4096 x 1536 (16 tokens, top-8 of 128) take 95 us against
-// 45 for the bytes.  (The copies and x without the products: 75 us; the products
-// with half the decode: 86.  Neither alone is the bound, and the registers allow
-// no more warps to overlap them.)
+// clock and SM); what bounds it is the decode, with the loads behind it.  A
+// weight costs 3.8 thread-instructions in all (1.0 mask, 0.6 multiplication, 0.1
+// shift, 0.6 scale, 0.13 MMA, the rest copies, x and addresses), the whole issue
+// 1.2 times the HBM rate: 82 experts of 4096 x 1536 (16 tokens, top-8 of 128)
+// take 95 us against 45 for the bytes, with 63% of the issue slots in use.  (When it took 99: copies and x
+// without the products 75, products with half the decode 86.  Neither alone is
+// the bound, and the registers allow no more warps to overlap them.)
 // The multiply-adds go to mma.sync (m16n8k16, BF16, f32 accumulation), 16
 // weight rows times up to 8 tokens per instruction: the tensor pipe is idle
 // otherwise (13% with them), and a second token costs no decode.  Measured
 // slower: more warps per SM (spills at 80 registers; 96 registers the same),
-// operands prefetched in registers instead of shared slots.
+// operands prefetched in registers instead of shared slots, a fourth slot (106
+// us: less L1 for x), first MMAs without a zeroed accumulator (one token
+// gate/up 9.6 instead of 9.3 us).
 //
 // Decode: a nibble's bits s|ee|m land in a BF16's sign, low exponent and top
 // mantissa bits, which reads as e2m1 * 2^-126 (its subnormal included); one
