@@ -8,9 +8,10 @@
 // weight costs 3.8 thread-instructions in all (1.0 mask, 0.6 multiplication, 0.1
 // shift, 0.6 scale, 0.13 MMA, the rest copies, x and addresses), the whole issue
 // 1.2 times the HBM rate: 82 experts of 4096 x 1536 (16 tokens, top-8 of 128)
-// take 95 us against 45 for the bytes, with 63% of the issue slots in use.  (When it took 99: copies and x
-// without the products 75, products with half the decode 86.  Neither alone is
-// the bound, and the registers allow no more warps to overlap them.)
+// take 95 us against 45 for the bytes, with 63% of the issue slots in use.
+// (When it took 99: copies and x without the products 75, products with half
+// the decode 86.  Neither alone is the bound, and the registers allow no more
+// warps to overlap them.)
 // The multiply-adds go to mma.sync (m16n8k16, BF16, f32 accumulation), 16
 // weight rows times up to 8 tokens per instruction: the tensor pipe is idle
 // otherwise (13% with them), and a second token costs no decode.  Measured
