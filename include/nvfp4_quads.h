@@ -622,8 +622,9 @@ NVFP4_API nvfp4_status moe_route_backward(const int32_t *topk_idx_dev, const flo
  *   MOE_EPI_COMBINE_F32  row = t*k_r + j; out f32 [T x ld_out]:
  *                        sum_j gate[t, j] y[t, j] in a fixed order (gate_dev
  *                        NULL: unweighted); written, not added, no atomics
- * expert_idx_dev int32 [T x k_r]; an index outside [0, E) gives zeros.  NULL:
- * one dense weight (E = 1, k_r = 1), eight tokens sharing each weight read.
+ * expert_idx_dev int32 [T x k_r]; an index outside [0, E) gives zeros (combined:
+ * its slot adds nothing, whatever its gate holds).  NULL: one dense weight (E =
+ * 1, k_r = 1), eight tokens sharing each weight read.
  * x_dev bf16 [rows x ldx]; codes, scales, s_t as nvfp4_qdq_weights writes
  * them for E tensors [N x K].  K % 64 == 0, any N (even for SwiGLU), ldx % 8
  * == 0, k_r <= 32; x, codes and scales 16-byte aligned.  Tokens that name the

@@ -507,10 +507,12 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
     }
 }
 
-// out[t, n] = sum_j gate[t, j] y[t k_r + j, n], in slot order.
+// out[t, n] = sum_j gate[t, j] y[t k_r + j, n], in slot order; a slot whose
+// expert does not exist takes no part, whatever its gate holds (as in the
+// one-launch form).
 __global__ void __launch_bounds__(THREADS) k_gemv_combine(const float *__restrict__ y, const float *__restrict__ gate,
-                                                          int64_t T, int k_r, int64_t N, float *__restrict__ out,
-                                                          int64_t ld_out)
+                                                          const int32_t *__restrict__ idx, int E, int k_r, int64_t N,
+                                                          float *__restrict__ out, int64_t ld_out)
 {
     const int64_t n = (int64_t)blockIdx.x * THREADS + threadIdx.x;
     const int64_t t = blockIdx.y;
@@ -518,7 +520,11 @@ __global__ void __launch_bounds__(THREADS) k_gemv_combine(const float *__restric
     grid_release();
     if (n >= N) return;
     float s = 0.0f;
-    for (int j = 0; j < k_r; ++j) s += (gate ? gate[t * k_r + j] : 1.0f) * y[(t * k_r + j) * N + n];
+    for (int j = 0; j < k_r; ++j) {
+        const int64_t pair = t * k_r + j;
+        if (idx && (idx[pair] < 0 || idx[pair] >= E)) continue;
+        s += (gate ? gate[pair] : 1.0f) * y[pair * N + n];
+    }
     out[t * ld_out + n] = s;
 }
 
@@ -642,7 +648,7 @@ extern "C" nvfp4_status moe_nvfp4_gemv(const void *x_dev, int64_t T, int64_t ldx
             launch_overlapped(k_nvfp4_gemv<STORE>, per_pair, THREADS, RING2, st, p, splits);
             if (check_launch("k_nvfp4_gemv") != NVFP4_OK) return NVFP4_ERR_CUDA;
             launch_overlapped(k_gemv_combine, dim3((unsigned)((N + THREADS - 1) / THREADS), (unsigned)tn), THREADS, 0, st,
-                              reinterpret_cast<const float *>(workspace), p.gate, tn, (int)k_r, N, out, ld_out);
+                              reinterpret_cast<const float *>(workspace), p.gate, p.idx, p.E, (int)k_r, N, out, ld_out);
         } else if (epilogue == MOE_EPI_SWIGLU_BF16) {
             launch_overlapped(k_nvfp4_gemv<SWIGLU>, per_pair, THREADS, RING2, st, p, splits);
         } else {

@@ -198,3 +198,45 @@ def test_long_sums(cuda):
     got = api.nvfp4_gemv(x, codes, sf, s, N, K)
     want = x.double() @ w.abs()[0].t()
     assert float(((got.double() - want).abs() / want).max()) <= (8 * 17 + 64 + 4 + 2) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("T,E,kr", [(2, 128, 8), (3, 128, 8), (4, 128, 8), (3, 128, 11)])
+def test_combine_of_a_few_tokens(cuda, T, E, kr):
+    """Two to four tokens on both sides of the form's border (T * k_r = E / 4):
+    every token has its own x, gates and output row."""
+    N, K = 97, 192
+    codes, sf, s, w = weights(30, E, N, K)
+    x = rnd(31, T * kr, K)
+    idx = torch.randint(0, E, (T, kr), generator=torch.Generator().manual_seed(32)).to(I32).to(cuda)
+    gate = torch.rand(T, kr, generator=torch.Generator().manual_seed(33)).to(cuda)
+    flat = idx.view(-1).long()
+    y = torch.bmm(w[flat], x.double()[:, :, None])[:, :, 0] * gate.double().view(-1, 1)
+    b = bound(K + kr, x.double(), w[flat]) * gate.double().view(-1, 1)
+    buf = torch.full((T, N + 6), 4.0, device=cuda)
+    api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_COMBINE_F32, gate=gate, out=buf[:, 1:1 + N])
+    want = y.view(T, kr, N).sum(1)
+    check(buf[:, 1:1 + N], want, b.view(T, kr, N).sum(1) + rounding(F32, want))
+    assert bool((buf[:, :1] == 4).all()) and bool((buf[:, 1 + N:] == 4).all())
+
+
+@pytest.mark.parametrize("T,E,kr", [(1, 8, 4), (2, 128, 8), (4, 128, 8), (2, 8, 4), (3, 128, 11), (300, 8, 4)])
+def test_combine_skips_experts_that_do_not_exist(cuda, T, E, kr):
+    """Such a slot adds nothing, whatever its gate and its row of x hold, in
+    every form."""
+    N, K = 40, 64
+    codes, sf, s, _ = weights(34, E, N, K)
+    x = rnd(35, T * kr, K)
+    idx = torch.randint(0, E, (T, kr), generator=torch.Generator().manual_seed(36)).to(I32).to(cuda)
+    gate = torch.rand(T, kr, generator=torch.Generator().manual_seed(37)).to(cuda)
+    gone = torch.rand(T, kr, generator=torch.Generator().manual_seed(38)).to(cuda) < 0.3
+    gone[0, 1], gone[-1, 0] = True, True
+    run = lambda: api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_COMBINE_F32, gate=gate)
+    gate[gone] = 0.0
+    want = run()
+    idx[gone] = torch.where(torch.arange(int(gone.sum()), device=cuda) % 2 == 0, -1, E).to(I32)
+    gate[gone] = float("nan")
+    gate[0, 1] = float("inf")
+    x[gone.view(-1)] = float("nan")
+    got = run()
+    assert bool(torch.isfinite(got).all())
+    assert torch.equal(got, want)        # the sums' order goes by the slots, missing ones included
