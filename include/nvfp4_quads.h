@@ -516,8 +516,9 @@ NVFP4_API nvfp4_status moe_w8a8_grouped_gemm(
  *   a            bf16: a_scales_dev NULL, a_dev [M x lda], row(r) = r,
  *                a_rows_dev NULL, T ignored; or kept in 8 bits (act8_quantize):
  *                a_dev uint8 codes [T x lda], a_scales_dev [T x ld_scales],
- *                row(r) = a_rows[r] (int32 [M]; an index outside [0, T) adds
- *                nothing), or r when a_rows_dev is NULL (T >= M).
+ *                row(r) = a_rows[r] (int32 [M]; a row whose index lies outside
+ *                [0, T) adds nothing, whatever g holds there), or r when
+ *                a_rows_dev is NULL (T >= M).
  *   out_dev      f32 or bf16 [E x N x K], contiguous; empty segments give 0.
  *                accumulate: the sum of old value and gradient in f32, rounded
  *                once to out's type.

@@ -42,8 +42,10 @@
 // expert, or rows nobody wrote.  Zeroing one operand would not do (0 * NaN), so
 // that stage lands on a barrier of its own CTA, warp 3 zeroes the surplus rows
 // of both operands in shared memory and only then reports the stage to the
-// MMA issuer.  Ragged rows (FWD, DGRAD) need nothing: a surplus row only makes
-// an accumulator column that the epilogue does not store.
+// MMA issuer.  A stage that holds a row whose index names no kept row goes the
+// same way: its row of a is zeros, but its row of g may be anything.  Ragged
+// rows (FWD, DGRAD) need nothing: a surplus row only makes an accumulator
+// column that the epilogue does not store.
 //
 // Long sums (WGRAD): the tensor core's f32 accumulation truncates, an error
 // that grows with the number of additions (1.6e-6 in norm after 1024 rows,
@@ -106,6 +108,8 @@ struct Params {
     int n_tiles;               // WGRAD: tiles along the N side
     int splits;                // WGRAD: row splits of every segment
     const int32_t *offsets;
+    const int32_t *a_rows;     // INDEXED: kept row of each row
+    int64_t kept_rows;         // INDEXED: rows of the kept tensor
     void *out;
     int64_t ld_out;
     int pairs;                 // bf16 out: two neighbouring columns may be stored at once
@@ -123,6 +127,7 @@ struct Shared {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    int dead[EPI_WARP0 + EPI_WARPS];   // INDEXED: the warp saw a row of no kept row
     int off[MAX_E + 1];        // segment bounds, made monotone and in [0, M]
     int tiles[MAX_E + 1];      // FWD / DGRAD: row tiles before expert e
 };
@@ -264,6 +269,43 @@ __device__ __forceinline__ Tile tile_at(const Params &p, const Shared *sh, const
     return w;
 }
 
+// Which rows of a stage (bit = row - its first one; rows from `end` on: none)
+// name no kept row; the same in all lanes.
+__device__ __forceinline__ uint64_t dead_rows(const Params &p, int row, int end)
+{
+    const int r = row + (int)(threadIdx.x & 31);
+    const int lo = r < end ? p.a_rows[r] : 0, hi = r + 32 < end ? p.a_rows[r + 32] : 0;
+    const unsigned dead_lo = __ballot_sync(0xffffffffu, r < end && (lo < 0 || lo >= p.kept_rows));
+    const unsigned dead_hi = __ballot_sync(0xffffffffu, r + 32 < end && (hi < 0 || hi >= p.kept_rows));
+    return (uint64_t)dead_hi << 32 | dead_lo;
+}
+
+// Is there such a row among this warp's share of all rows?  16-byte loads, eight
+// under way, between the ends.
+__device__ __forceinline__ bool any_dead_row(const Params &p, int share, int shares)
+{
+    const int lane = threadIdx.x & 31;
+    const auto gone = [&](int v) { return v < 0 || v >= p.kept_rows; };
+    const int64_t head = min(p.M, (int64_t)((16 - (reinterpret_cast<uintptr_t>(p.a_rows) & 15u)) & 15u) / 4);
+    const int64_t vecs = (p.M - head) / 4, done = head + vecs * 4;
+    const int4 *body = reinterpret_cast<const int4 *>(p.a_rows + head);
+    bool dead = false;
+    if (share == 0) {
+        if (lane < head) dead = gone(p.a_rows[lane]);
+        if (done + lane < p.M) dead = dead || gone(p.a_rows[done + lane]);
+    }
+    constexpr int DEEP = 8;
+    const int64_t step = (int64_t)shares * 32;
+    for (int64_t i = (int64_t)share * 32 + lane; i < vecs; i += DEEP * step) {
+        int4 v[DEEP];
+#pragma unroll
+        for (int j = 0; j < DEEP; ++j) v[j] = body[min(i + j * step, vecs - 1)];
+#pragma unroll
+        for (int j = 0; j < DEEP; ++j) dead |= gone(v[j].x) | gone(v[j].y) | gone(v[j].z) | gone(v[j].w);
+    }
+    return __any_sync(0xffffffffu, dead ? 1 : 0) != 0;
+}
+
 // WGRAD's epilogue holds 128 sums and 32 columns in flight per thread: the
 // control warps pass registers on (56 + 2 x 224 of the 3 x 168 per warpgroup
 // that the block starts with).
@@ -338,7 +380,8 @@ __device__ __forceinline__ void store_rows(const Params &p, __nv_bfloat16 *out, 
     }
 }
 
-template <int MODE, typename OutT, bool ADD>
+// INDEXED (WGRAD): rows may name no kept row (a_rows).
+template <int MODE, typename OutT, bool ADD, bool INDEXED>
 __global__ void __launch_bounds__(THREADS, 1)
 k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ CUtensorMap tm_n, const Params p)
 {
@@ -422,12 +465,21 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
             pre += cnt[i];
         }
         if (lane == 31 && p.E == MAX_E) { sh->off[MAX_E] = last; sh->tiles[MAX_E] = incl; }
+        if (INDEXED && lane == 0) sh->dead[warp] = 0;
+    } else if (INDEXED) {
+        // the other warps look through the row index meanwhile: a routed batch
+        // without padding has no dead row, and then no stage looks again
+        const bool dead = any_dead_row(p, warp < FIX_WARP ? warp : warp - 1, EPI_WARP0 + EPI_WARPS - 1);
+        if (lane == 0) sh->dead[warp] = dead;
     }
     grid_release();
     ptx::tc_fence_before();
     ptx::cluster_sync();                   // barriers of both CTAs initialized before any remote use
     ptx::tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sh->tmem_base, 0);
+    // looking at every stage's rows costs loads that queue behind the epilogue's stores
+    bool look = false;
+    if (INDEXED) look = __any_sync(0xffffffffu, lane < EPI_WARP0 + EPI_WARPS && sh->dead[lane] != 0) != 0;
     const int total = MODE == WGRAD ? p.E * p.m_tiles * p.n_tiles * p.splits : sh->tiles[p.E] * p.m_tiles;
 
     if (warp == PROD_M_WARP || warp == PROD_N_WARP) {
@@ -451,6 +503,9 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                 const int mn = (int)(m_side ? w.m0 + rank * 128 : w.n0 + (int)rank * half_n);
                 const uint32_t bytes = m_side || MODE == WGRAD ? OPER_BYTES : (uint32_t)half_n * (BK * 2);
                 for (int kb = 0; kb < w.stages; ++kb) {
+                    const int row = w.r0 + kb * BK;
+                    bool fix = MODE == WGRAD && row + BK > w.r1;
+                    if (INDEXED && look) fix = dead_rows(p, row, w.r1) != 0 || fix;
                     if (!wait_bar(ptx::smem_u32(&sh->empty[stage]), phase ^ 1u, abort_flag, p)) {
                         ok = false;
                         break;
@@ -458,9 +513,8 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     const uint32_t dst = ptx::smem_u32(stage_base + stage * STAGE_BYTES + (m_side ? 0 : OPER_BYTES));
                     const uint32_t fb = ptx::smem_u32(&sh->full[stage]);
                     const uint32_t lfb = ptx::mapa_shared(fb, 0);      // the leader's barrier
-                    const int row = w.r0 + kb * BK;
-                    if (MODE == WGRAD && row + BK > w.r1) {
-                        // ragged: land in this CTA, the fixer reports it
+                    if (fix) {
+                        // rows to zero: land in this CTA, the fixer reports it
                         const uint32_t rb = ptx::smem_u32(&sh->raw[stage]);
                         if (one) {
                             ptx::mbar_arrive_expect_tx(rb, OPER_BYTES);
@@ -575,27 +629,45 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
     } else if (warp == FIX_WARP) {
         give_registers<MODE>();
         if (MODE == WGRAD) {
-            // --------------------- zero the surplus rows of ragged stages
+            // --------------------- zero surplus rows, and rows of no kept row
             uint32_t stage = 0, parity = 0;             // one parity bit per stage's raw barrier
-            for (Walk<MODE> at(p, unit, n_units); at.t < total; at.next(p, n_units)) {
+            bool ok = true;
+            for (Walk<MODE> at(p, unit, n_units); ok && at.t < total; at.next(p, n_units)) {
                 const Tile w = tile_at<MODE>(p, sh, at);
-                if (w.stages == 0) continue;
-                const uint32_t s = (stage + (uint32_t)(w.stages - 1)) % STAGES;
-                stage = (s + 1) % STAGES;
-                const int rows = (w.r1 - w.r0) - (w.stages - 1) * BK;
-                if (rows == BK) continue;
-                if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p)) break;
-                parity ^= 1u << s;
-                uint8_t *base = stage_base + s * STAGE_BYTES;
-                // 128-byte rows `rows`..63 of both operands' boxes; the swizzle stays inside a row
-                for (int i = lane; i < (BK - rows) * 8; i += 32) {
+                // without such rows only a segment's last stage can need it
+                int kb = INDEXED && look ? 0 : max(0, w.stages - 1);
+                stage = (stage + (uint32_t)kb) % STAGES;
+                for (; kb < w.stages; ++kb) {
+                    const uint32_t s = stage;
+                    if (++stage == STAGES) stage = 0;
+                    const int row = w.r0 + kb * BK;
+                    uint64_t zero = 0;
+                    if (INDEXED && look) zero = dead_rows(p, row, w.r1);
+                    if (row + BK > w.r1) zero |= ~0ull << (w.r1 - row);
+                    if (zero == 0) continue;
+                    if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p)) {
+                        ok = false;
+                        break;
+                    }
+                    parity ^= 1u << s;
+                    uint8_t *base = stage_base + s * STAGE_BYTES;
+                    // 128-byte rows of both operands' boxes; the swizzle stays inside a row
+                    const int first = __ffsll((long long)zero) - 1;
+                    const auto zero_16 = [&](int i) {
 #pragma unroll
-                    for (int b = 0; b < 4; ++b)
-                        *reinterpret_cast<uint4 *>(base + b * BOX_BYTES + rows * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+                        for (int b = 0; b < 4; ++b)
+                            *reinterpret_cast<uint4 *>(base + b * BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+                    };
+                    if (!INDEXED || zero == ~0ull << first) {
+                        for (int i = 8 * first + lane; i < BK * 8; i += 32) zero_16(i);
+                    } else {
+                        for (int i = 8 * first + lane; i < BK * 8; i += 32)
+                            if (zero >> (i >> 3) & 1) zero_16(i);
+                    }
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0));
                 }
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0));
             }
         }
     } else {
@@ -718,13 +790,13 @@ __global__ void __launch_bounds__(256) k_wgrad_reduce(const float *__restrict__ 
 
 // ----------------------------------------------------------------- host side
 
-template <int MODE, typename OutT, bool ADD>
+template <int MODE, typename OutT, bool ADD, bool INDEXED = false>
 static nvfp4_status launch(const CUtensorMap &tm_m, const CUtensorMap &tm_n, const Params &p, int64_t max_tiles,
                            cudaStream_t st)
 {
     static std::once_flag once[64];
     static cudaError_t attr_err[64];
-    auto kern = k_ragged_gemm<MODE, OutT, ADD>;
+    auto kern = k_ragged_gemm<MODE, OutT, ADD, INDEXED>;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return check_launch("k_ragged_gemm: device");
     std::call_once(once[dev], [&] {
@@ -748,6 +820,14 @@ static nvfp4_status launch(const CUtensorMap &tm_m, const CUtensorMap &tm_n, con
     cfg.numAttrs = 2;
     cudaLaunchKernelEx(&cfg, kern, tm_m, tm_n, p);
     return check_launch("k_ragged_gemm");
+}
+
+template <typename OutT, bool ADD>
+static nvfp4_status launch_wgrad(const CUtensorMap &tm_m, const CUtensorMap &tm_n, const Params &p, int64_t max_tiles,
+                                 cudaStream_t st)
+{
+    return p.a_rows ? launch<WGRAD, OutT, ADD, true>(tm_m, tm_n, p, max_tiles, st)
+                    : launch<WGRAD, OutT, ADD, false>(tm_m, tm_n, p, max_tiles, st);
 }
 
 // Rows of bf16 pairs on 4 bytes?
@@ -922,18 +1002,20 @@ extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t
     p.splits = splits;
     p.wait_limit_ns = TIMEOUT_NS;
     p.offsets = offsets_dev;
+    p.a_rows = a_rows_dev;
+    p.kept_rows = T;
     p.out = splits > 1 ? partials : out_dev;
     p.ld_out = K;
     p.pairs = pair_stores(p.out, K);
     p.dev_status = dev_status;
     if (splits == 1) {
         if (out_f32)
-            return accumulate ? launch<WGRAD, float, true>(tm_m, tm_n, p, max_tiles, st)
-                              : launch<WGRAD, float, false>(tm_m, tm_n, p, max_tiles, st);
-        return accumulate ? launch<WGRAD, __nv_bfloat16, true>(tm_m, tm_n, p, max_tiles, st)
-                          : launch<WGRAD, __nv_bfloat16, false>(tm_m, tm_n, p, max_tiles, st);
+            return accumulate ? launch_wgrad<float, true>(tm_m, tm_n, p, max_tiles, st)
+                              : launch_wgrad<float, false>(tm_m, tm_n, p, max_tiles, st);
+        return accumulate ? launch_wgrad<__nv_bfloat16, true>(tm_m, tm_n, p, max_tiles, st)
+                          : launch_wgrad<__nv_bfloat16, false>(tm_m, tm_n, p, max_tiles, st);
     }
-    const nvfp4_status rc = launch<WGRAD, float, false>(tm_m, tm_n, p, max_tiles, st);
+    const nvfp4_status rc = launch_wgrad<float, false>(tm_m, tm_n, p, max_tiles, st);
     if (rc != NVFP4_OK) return rc;
     const int64_t n = (int64_t)E * N * K;
     const unsigned blocks = (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, (int64_t)num_sms() * 8));

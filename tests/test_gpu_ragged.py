@@ -365,3 +365,62 @@ def test_bounded_wait_expiry_reports_timeout(cuda):
     got = api.ragged_gemm(a, w, off, out_dtype=F32)
     y, s = ref_rows(a, w, off, False, torch.zeros(100, 200, device=cuda))
     check(got, y, sum_bound(128, s) + rounding(F32, y))
+
+
+@pytest.mark.parametrize("counts,N,K", [([64], 8, 8), ([1, 64, 0, 130], 264, 72), ([300, 1, 700], 520, 328),
+                                        ([2000, 0, 3, 64], 136, 256)], ids=str)
+def test_rows_of_no_kept_row_add_nothing(cuda, counts, N, K):
+    """Rows whose index lies outside the kept tensor, with Inf and NaN in g:
+    alone in a stage, whole stages of them, a segment without any other, the
+    last rows of a segment."""
+    E, M, T = len(counts), sum(counts) + 5, 40
+    off = offsets_of(counts, cuda, start=2)
+    a8 = api.act8_quantize(rnd(81, T, -(-K // 8) * 8)[:, :K])
+    gen = torch.Generator().manual_seed(82)
+    g = rnd(83, M, N, scale=0.1)
+    for pick in ("few", "stage", "segment", "ends", "all"):
+        rows = torch.randint(0, T, (M,), generator=gen).to(I32).to(cuda)
+        gone = torch.zeros(M, dtype=torch.bool, device=cuda)
+        if pick == "few":
+            gone = (torch.rand(M, generator=gen) < 0.02).to(cuda)
+            gone[2 + counts[0] // 2] = True
+        elif pick == "stage":
+            gone[2:66] = True
+            gone[-70:-6] = True
+        elif pick == "segment":
+            gone[int(off[-2]):int(off[-1])] = True
+        elif pick == "ends":
+            gone[(off[1:].long() - 1).clamp_min(0)] = True
+            gone[off[:-1].long()] = True
+        else:
+            gone[:] = True
+        rows[gone] = torch.where(torch.arange(int(gone.sum()), device=cuda) % 2 == 0, -1, T).to(I32)
+        bad = g.clone()
+        bad[gone] = float("nan")
+        bad[gone.nonzero()[::3, 0]] = float("inf")
+        full = torch.zeros(M, K, dtype=torch.float64, device=cuda)
+        full[~gone] = kept_values(a8)[rows[~gone].long()]
+        y, s = ref_wgrad(torch.where(gone[:, None], torch.zeros_like(g), g), full, off)
+        got = api.ragged_wgrad(bad, a8, off, a_rows=rows)
+        check(got, y, sum_bound(max(counts) + 1, s) + rounding(F32, y), pick)
+
+
+def test_rows_of_no_kept_row_in_split_segments(cuda):
+    """The same where rows are split over the SMs, and added to an old value."""
+    M, T, N, K = 6000, 50, 72, 96
+    off = torch.tensor([10, 2500, 5990], dtype=I32, device=cuda)
+    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, 2, 1) > M * K * 2
+    a8 = api.act8_quantize(rnd(84, T, K))
+    gen = torch.Generator().manual_seed(85)
+    rows = torch.randint(-3, T + 3, (M,), generator=gen).to(I32).to(cuda)
+    gone = (rows < 0) | (rows >= T)
+    g = rnd(86, M, N, scale=0.1)
+    full = torch.zeros(M, K, dtype=torch.float64, device=cuda)
+    full[~gone] = kept_values(a8)[rows[~gone].long()]
+    g[gone] = 0
+    y, s = ref_wgrad(g, full, off)
+    g[gone] = float("nan")
+    old = rnd(87, 2, N, K).float()
+    got = api.ragged_wgrad(g, a8, off, a_rows=rows, out=old.clone(), accumulate=True)
+    z = y + old.double()
+    check(got, z, sum_bound(3500, s) + ULP_ADD * (y.abs() + old.double().abs()) + rounding(F32, z))
