@@ -276,17 +276,20 @@ class MoELayerW4A16:
         return self.y
 
     def _train_buffers(self, dev):
-        """Routed rows of the training pair, made at the first forward_train."""
+        """Buffers of the training pair, made at the first forward_train: all of
+        them or, where memory runs out, none."""
         m, H, I = self.T * self.k_r, self.H, self.I
         bf = dict(dtype=torch.bfloat16, device=dev)
-        self.rows_h = torch.empty(m, H, **bf)           # routed X, later routed dY
-        self.rows_y = torch.empty(m, H, **bf)           # down rows, later dX rows
-        self.y13 = torch.empty(m, 2 * I, **bf)          # gate/up rows, later their gradient
-        self.h_t = torch.empty(m, I, **bf)              # h, later its gradient
-        self.gh = torch.empty(m, I, **bf)               # router-weighted h
-        self.dgate = torch.empty(m, dtype=torch.float32, device=dev)
-        self.x8 = api.Act8.empty(self.T, H, dev)       # kept between forward_train and backward
-        self.y8 = api.Act8.empty(m, 2 * I, dev)
+        made = dict(
+            rows_h=torch.empty(m, H, **bf),             # routed X, later routed dY
+            rows_y=torch.empty(m, H, **bf),             # down rows, later dX rows
+            y13=torch.empty(m, 2 * I, **bf),            # gate/up rows, later their gradient
+            h_t=torch.empty(m, I, **bf),                # h, later its gradient
+            gh=torch.empty(m, I, **bf),                 # router-weighted h
+            dgate=torch.empty(m, dtype=torch.float32, device=dev),
+            x8=api.Act8.empty(self.T, H, dev),          # kept between forward_train and backward
+            y8=api.Act8.empty(m, 2 * I, dev))
+        self.__dict__.update(made)
 
     def forward_train(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """The layer with what backward needs kept in 8 bits: X (per token, not

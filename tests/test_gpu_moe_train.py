@@ -276,3 +276,25 @@ def test_nothing_kept_after_a_failed_forward_or_new_weights(cuda, monkeypatch):
     lay.set_weights(w13, w2)
     with pytest.raises(RuntimeError, match="no forward_train"):
         lay.backward(dy)
+
+
+def test_forward_train_after_one_without_memory(cuda, monkeypatch):
+    """A first call whose buffers do not fit can be made again."""
+    from quantization_nvfp4_quantize_b200 import api
+    lay, _, _ = layer(MoELayerW4A16, 8, 4, 64, 64, 2)
+    x, logits = rnd(1, 8, 64), rnd(2, 8, 4, dtype=torch.float32)
+    real, calls = api.Act8.empty, []
+
+    def second_fails(*a):
+        calls.append(a)
+        if len(calls) == 2:
+            raise torch.OutOfMemoryError("no memory")
+        return real(*a)
+
+    with monkeypatch.context() as m:
+        m.setattr(api.Act8, "empty", staticmethod(second_fails))
+        with pytest.raises(torch.OutOfMemoryError):
+            lay.forward_train(x, logits)
+    y = lay.forward_train(x, logits)
+    assert torch.equal(y, layer(MoELayerW4A16, 8, 4, 64, 64, 2)[0].forward_train(x, logits))
+    lay.backward(rnd(3, 8, 64))

@@ -308,3 +308,26 @@ def test_backward_refuses_destinations_before_any_call():
     with pytest.raises(ValueError, match="x must be bf16"):
         t.forward_train(x, logits)
     assert t.train_routing is not None          # a refused call leaves what was kept
+
+
+def test_training_buffers_are_made_together(monkeypatch):
+    """One that cannot be allocated leaves the layer as it was, and the next
+    try makes all of them."""
+    from quantization_nvfp4_quantize_b200.moe import MoELayerW4A16
+    t = MoELayerW4A16.__new__(MoELayerW4A16)
+    t.T, t.H, t.E, t.k_r, t.I = 2, 64, 4, 2, 32
+    before = dict(t.__dict__)
+    real = api.Act8.empty
+
+    def full(M, K, device):
+        if M == 4:                               # the gate/up rows
+            raise torch.OutOfMemoryError("no memory")
+        return real(M, K, device)
+
+    with monkeypatch.context() as m:
+        m.setattr(api.Act8, "empty", staticmethod(full))
+        with pytest.raises(torch.OutOfMemoryError):
+            t._train_buffers("cpu")
+    assert t.__dict__ == before
+    t._train_buffers("cpu")
+    assert tuple(t.x8.codes.shape) == (2, 64) and tuple(t.y8.codes.shape) == (4, 64) and tuple(t.gh.shape) == (4, 32)
