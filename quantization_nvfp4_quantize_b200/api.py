@@ -159,20 +159,30 @@ def padded_rows_bound(T: int, k_r: int, E: int, seg_align: int = 128) -> int:
     return -(-(T * k_r + E * (seg_align - 1)) // seg_align) * seg_align
 
 
-def route(logits: torch.Tensor, k_r: int, m_pad_max: int | None = None, seg_align: int = 128) -> Routing:
+def empty_routing(T: int, k_r: int, E: int, device, m_pad_max: int | None = None, seg_align: int = 128) -> Routing:
+    """Buffers of a routing of T tokens, for route's `out`."""
+    if m_pad_max is None:
+        m_pad_max = padded_rows_bound(T, k_r, E, seg_align)
+    return Routing(torch.empty(T, k_r, dtype=I32, device=device), torch.empty(T, k_r, dtype=F32, device=device),
+                   torch.empty(E + 1, dtype=I32, device=device), torch.empty(T, k_r, dtype=I32, device=device),
+                   torch.empty(m_pad_max, dtype=I32, device=device), torch.empty(m_pad_max, dtype=F32, device=device),
+                   m_pad_max, seg_align)
+
+
+def route(logits: torch.Tensor, k_r: int, m_pad_max: int | None = None, seg_align: int = 128, *,
+          out: Routing | None = None, workspace: torch.Tensor | None = None) -> Routing:
+    """moe_route (see the header) on f32 logits [T, E].  `out` (empty_routing of
+    the same sizes; its m_pad_max and seg_align are used) and `workspace` keep
+    the call free of allocations."""
     lib = _lib.load()
     assert logits.dtype == F32 and logits.is_contiguous()
     T, E = logits.shape
     dev = logits.device
-    if m_pad_max is None:
-        m_pad_max = padded_rows_bound(T, k_r, E, seg_align)
-    r = Routing(torch.empty(T, k_r, dtype=I32, device=dev), torch.empty(T, k_r, dtype=F32, device=dev),
-                torch.empty(E + 1, dtype=I32, device=dev), torch.empty(T, k_r, dtype=I32, device=dev),
-                torch.empty(m_pad_max, dtype=I32, device=dev), torch.empty(m_pad_max, dtype=F32, device=dev),
-                m_pad_max, seg_align)
-    ws = _ws(lib.moe_route_workspace_size(T, E), dev)
-    check(lib.moe_route(_p(logits), T, E, k_r, _p(r.topk_idx), _p(r.topk_gate), seg_align, _p(r.offsets), _p(r.dst_row),
-                        _p(r.row_token), _p(r.row_gate), m_pad_max, _p(ws), ws.numel(), _stream(dev)))
+    r = empty_routing(T, k_r, E, dev, m_pad_max, seg_align) if out is None else out
+    assert tuple(r.topk_idx.shape) == (T, k_r) and r.offsets.numel() == E + 1
+    ws = _ws(lib.moe_route_workspace_size(T, E), dev) if workspace is None else workspace
+    check(lib.moe_route(_p(logits), T, E, k_r, _p(r.topk_idx), _p(r.topk_gate), r.seg_align, _p(r.offsets), _p(r.dst_row),
+                        _p(r.row_token), _p(r.row_gate), r.m_pad_max, _p(ws), ws.numel(), _stream(dev)))
     return r
 
 

@@ -287,15 +287,20 @@ class MoELayerW4A16:
             h_t=torch.empty(m, I, **bf),                # h, later its gradient
             gh=torch.empty(m, I, **bf),                 # router-weighted h
             dgate=torch.empty(m, dtype=torch.float32, device=dev),
-            x8=api.Act8.empty(self.T, H, dev),          # kept between forward_train and backward
-            y8=api.Act8.empty(m, 2 * I, dev))
+            # kept between forward_train and backward: the routing beside the rows
+            # it belongs to, so that a replayed graph's forward writes all of it
+            x8=api.Act8.empty(self.T, H, dev),
+            y8=api.Act8.empty(m, 2 * I, dev),
+            kept_routing=api.empty_routing(self.T, self.k_r, self.E, dev, seg_align=1),
+            ws_kept=api._ws(api._lib.load().moe_route_workspace_size(self.T, self.E), dev))
         self.__dict__.update(made)
 
     def forward_train(self, x: torch.Tensor, logits: torch.Tensor) -> torch.Tensor:
         """The layer with what backward needs kept in 8 bits: X (per token, not
         per routed copy) and the gate/up rows.  Returns Y f32 [T, H], a new
-        tensor.  I must be a multiple of 32.  After a call that fails on its way
-        nothing is kept."""
+        tensor.  I must be a multiple of 32.  What is kept lives in the layer's
+        buffers: a later call, or a replayed graph that holds one, takes its
+        place.  After a call that fails on its way nothing is kept."""
         if tuple(x.shape) != (self.T, self.H) or tuple(logits.shape) != (self.T, self.E):
             raise ValueError(f"forward_train: need x [{self.T}, {self.H}] and logits [{self.T}, {self.E}], got "
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
@@ -306,7 +311,7 @@ class MoELayerW4A16:
             self._train_buffers(x.device)
         self.train_routing = None
         with _current(x.device):
-            r = api.route(logits, self.k_r, seg_align=1)
+            r = api.route(logits, self.k_r, out=self.kept_routing, workspace=self.ws_kept)
             api.act8_quantize(x, out=self.x8)
             api.routed_rows_bf16(x, r.row_token, r.m_pad_max, out=self.rows_h)
             api.ragged_gemm(self.rows_h, self.wq13, r.offsets, out=self.y13)
@@ -318,8 +323,8 @@ class MoELayerW4A16:
 
     def backward(self, dy: torch.Tensor, *, dw13: torch.Tensor | None = None, dw2: torch.Tensor | None = None,
                  accumulate: bool = False) -> LayerGrads:
-        """Gradients of the last forward_train for dY (bf16 [T, H]), with its
-        weights (call it before set_weights).  dw13 / dw2: where the weight
+        """Gradients of the last forward_train, called or replayed, for dY (bf16
+        [T, H]), with its weights (call it before set_weights).  dw13 / dw2: where the weight
         gradients go (f32 or bf16, contiguous); accumulate adds to them.  A
         refused call changes neither."""
         r = self.train_routing

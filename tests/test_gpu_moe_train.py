@@ -298,3 +298,34 @@ def test_forward_train_after_one_without_memory(cuda, monkeypatch):
     y = lay.forward_train(x, logits)
     assert torch.equal(y, layer(MoELayerW4A16, 8, 4, 64, 64, 2)[0].forward_train(x, logits))
     lay.backward(rnd(3, 8, 64))
+
+
+def test_backward_follows_a_replayed_forward(cuda):
+    """Routing and kept rows change together: backward after the replay of a
+    captured forward_train gives that forward's gradients, whatever was called
+    in between, and so does a captured backward after an eager forward."""
+    T, E, H, I, kr = 64, 8, 128, 64, 2
+    lay, _, _ = layer(MoELayerW4A16, T, E, H, I, kr)
+    data = [(rnd(60 + i, T, H), rnd(70 + i, T, E, dtype=torch.float32)) for i in range(2)]
+    dy = rnd(80, T, H)
+    want = []
+    for x, logits in data:
+        lay.forward_train(x, logits)
+        want.append(lay.backward(dy))
+    fwd, bwd = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(fwd):
+        lay.forward_train(*data[0])
+    with torch.cuda.graph(bwd):
+        g = lay.backward(dy)
+
+    def same(a, b):
+        return all(torch.equal(getattr(a, n), getattr(b, n)) for n in ("dx", "dlogits", "dw13", "dw2"))
+
+    lay.forward_train(*data[1])
+    fwd.replay()
+    assert same(lay.backward(dy), want[0])
+    bwd.replay()
+    assert same(g, want[0])
+    lay.forward_train(*data[1])
+    bwd.replay()
+    assert same(g, want[1]) and same(lay.backward(dy), want[1])
