@@ -14,7 +14,7 @@ import dataclasses
 import torch
 
 from . import _lib
-from ._lib import check
+from ._lib import Nvfp4Error, check
 
 U8 = torch.uint8
 I32 = torch.int32

@@ -209,6 +209,7 @@ class LayerGrads:
     dlogits: torch.Tensor       # [T, E]
     dw13: torch.Tensor          # [E, 2I, H], of the fake-quantized weights (straight through to the bf16 ones)
     dw2: torch.Tensor           # [E, H, I]
+    status: torch.Tensor | None = None   # int32 [1], the layer's status word: see MoELayerW4A16.check_status
 
 
 class MoELayerW4A16:
@@ -225,7 +226,8 @@ class MoELayerW4A16:
 
     forward_train / backward are the training step's pair: unpadded ragged
     segments, X and the SwiGLU's inputs kept in 8 bits in between, no atomics
-    (the same inputs give the same bits).
+    (the same inputs give the same bits).  A bounded wait of their kernels that
+    runs out is reported in a status word only: check_status reads it.
     """
 
     def __init__(self, w13: torch.Tensor, w2: torch.Tensor, tokens: int, topk: int, seg_align: int = 256):
@@ -248,6 +250,7 @@ class MoELayerW4A16:
         self.h = torch.empty(self.m_pad, I, dtype=torch.bfloat16, device=dev)
         self.y = torch.empty(tokens, H, dtype=torch.float32, device=dev)
         self.routing = None
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
 
     def set_weights(self, w13: torch.Tensor, w2: torch.Tensor):
         """Fake-quantize new bf16 weights into the layer (the per-step work of
@@ -300,7 +303,8 @@ class MoELayerW4A16:
         per routed copy) and the gate/up rows.  Returns Y f32 [T, H], a new
         tensor.  I must be a multiple of 32.  What is kept lives in the layer's
         buffers: a later call, or a replayed graph that holds one, takes its
-        place.  After a call that fails on its way nothing is kept."""
+        place.  After a call that fails on its way nothing is kept; a kernel
+        that gave up waiting shows in check_status only."""
         if tuple(x.shape) != (self.T, self.H) or tuple(logits.shape) != (self.T, self.E):
             raise ValueError(f"forward_train: need x [{self.T}, {self.H}] and logits [{self.T}, {self.E}], got "
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
@@ -314,9 +318,9 @@ class MoELayerW4A16:
             r = api.route(logits, self.k_r, out=self.kept_routing, workspace=self.ws_kept)
             api.act8_quantize(x, out=self.x8)
             api.routed_rows_bf16(x, r.row_token, r.m_pad_max, out=self.rows_h)
-            api.ragged_gemm(self.rows_h, self.wq13, r.offsets, out=self.y13)
+            api.ragged_gemm(self.rows_h, self.wq13, r.offsets, out=self.y13, dev_status=self.status)
             api.swiglu_act8(self.y13, h=self.h_t, out=self.y8)
-            api.ragged_gemm(self.h_t, self.wq2, r.offsets, out=self.rows_y)
+            api.ragged_gemm(self.h_t, self.wq2, r.offsets, out=self.rows_y, dev_status=self.status)
             y = api.combine_rows(self.rows_y, r.dst_row, gate=r.topk_gate)
         self.train_routing = r
         return y
@@ -326,7 +330,9 @@ class MoELayerW4A16:
         """Gradients of the last forward_train, called or replayed, for dY (bf16
         [T, H]), with its weights (call it before set_weights).  dw13 / dw2: where the weight
         gradients go (f32 or bf16, contiguous); accumulate adds to them.  A
-        refused call changes neither."""
+        refused call changes neither; one that fails on its way (no memory for
+        a workspace) may have written the first of them, and check_status tells
+        whether both are complete."""
         r = self.train_routing
         if r is None:
             raise RuntimeError("backward: no forward_train to differentiate")
@@ -346,14 +352,28 @@ class MoELayerW4A16:
         with _current(dy.device):
             # routed dY; u = dY W2, the gradient of h before the router's weight
             api.routed_rows_bf16(dy, r.row_token, r.m_pad_max, out=self.rows_h)
-            api.ragged_gemm(self.rows_h, self.wq2, r.offsets, transpose=True, out=self.h_t)
+            api.ragged_gemm(self.rows_h, self.wq2, r.offsets, transpose=True, out=self.h_t, dev_status=self.status)
             api.swiglu_act8_backward(self.y8, self.h_t, row_gate=r.row_gate, dy=self.y13, gh=self.gh, dgate=self.dgate)
-            dw2 = api.ragged_wgrad(self.rows_h, self.gh, r.offsets, out=dw2, accumulate=accumulate)
-            dw13 = api.ragged_wgrad(self.y13, self.x8, r.offsets, a_rows=r.row_token, out=dw13, accumulate=accumulate)
-            api.ragged_gemm(self.y13, self.wq13, r.offsets, transpose=True, out=self.rows_y)
+            dw2 = api.ragged_wgrad(self.rows_h, self.gh, r.offsets, out=dw2, accumulate=accumulate, dev_status=self.status)
+            dw13 = api.ragged_wgrad(self.y13, self.x8, r.offsets, a_rows=r.row_token, out=dw13, accumulate=accumulate,
+                                    dev_status=self.status)
+            api.ragged_gemm(self.y13, self.wq13, r.offsets, transpose=True, out=self.rows_y, dev_status=self.status)
             dx = api.combine_rows(self.rows_y, r.dst_row)
             dlogits = api.route_backward(r.topk_idx, r.topk_gate, r.dst_row, self.dgate, self.E)
-        return LayerGrads(dx, dlogits, dw13, dw2)
+        return LayerGrads(dx, dlogits, dw13, dw2, self.status)
+
+    def check_status(self):
+        """Raises Nvfp4Error if a wait ran out in a forward_train or backward
+        since the last check: their results, and gradients they were added to,
+        are then incomplete, and nothing is kept.  Waits for the current stream;
+        call it before an optimizer step uses the gradients."""
+        with _current(self.status.device):
+            status = api.read_status(self.status)
+            if status == 0:
+                return
+            self.status.zero_()
+        self.train_routing = None
+        raise api.Nvfp4Error(status, "a kernel of the training pair gave up waiting; drop the step's results and gradients")
 
     _route_into = MoELayerW4A4._route_into
 

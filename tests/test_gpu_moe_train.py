@@ -329,3 +329,23 @@ def test_backward_follows_a_replayed_forward(cuda):
     lay.forward_train(*data[1])
     bwd.replay()
     assert same(g, want[1]) and same(lay.backward(dy), want[1])
+
+
+def test_status_of_a_step(cuda):
+    """A clean step leaves the word at 0; one that a wait marked is reported."""
+    from quantization_nvfp4_quantize_b200._lib import Nvfp4Error
+    lay, _, _ = layer(MoELayerW4A16, 8, 4, 64, 64, 2)
+    x, logits, dy = rnd(1, 8, 64), rnd(2, 8, 4, dtype=torch.float32), rnd(3, 8, 64)
+    lay.forward_train(x, logits)
+    g = lay.backward(dy)
+    lay.check_status()
+    assert int(g.status) == 0
+    lay.status.fill_(5)
+    with pytest.raises(Nvfp4Error, match="TIMEOUT"):
+        lay.check_status()
+    lay.check_status()
+    with pytest.raises(RuntimeError, match="no forward_train"):
+        lay.backward(dy)
+    lay.forward_train(x, logits)
+    assert torch.equal(lay.backward(dy).dx, g.dx)
+    lay.check_status()

@@ -331,3 +331,43 @@ def test_training_buffers_are_made_together(monkeypatch):
     assert t.__dict__ == before
     t._train_buffers("cpu")
     assert tuple(t.x8.codes.shape) == (2, 64) and tuple(t.y8.codes.shape) == (4, 64) and tuple(t.gh.shape) == (4, 32)
+
+
+def test_training_pair_reports_waits_that_ran_out(monkeypatch):
+    """Every call that can give up waiting gets the layer's status word;
+    check_status raises for it once and keeps nothing."""
+    import contextlib
+
+    from quantization_nvfp4_quantize_b200 import moe
+    bf = dict(dtype=torch.bfloat16)
+    t = moe.MoELayerW4A16.__new__(moe.MoELayerW4A16)
+    t.T, t.H, t.E, t.k_r, t.I, t.train_routing = 2, 64, 4, 2, 32, None
+    t.wq13, t.wq2 = torch.zeros(4, 64, 64, **bf), torch.zeros(4, 64, 32, **bf)
+    t.status = torch.zeros(1, dtype=torch.int32)
+    seen = []
+
+    def fake(name, result):
+        def call(*args, **kw):
+            seen.append((name, kw.get("dev_status")))
+            return result
+        return call
+
+    monkeypatch.setattr(moe, "_current", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(api, "route", lambda logits, k_r, **kw: kw["out"])
+    monkeypatch.setattr(api, "read_status", lambda word: int(word))
+    for name in ("act8_quantize", "routed_rows_bf16", "swiglu_act8", "swiglu_act8_backward", "combine_rows",
+                 "route_backward"):
+        monkeypatch.setattr(api, name, lambda *a, **kw: torch.zeros(1))
+    for name in ("ragged_gemm", "ragged_wgrad"):
+        monkeypatch.setattr(api, name, fake(name, torch.zeros(1)))
+    t.forward_train(torch.zeros(2, 64, **bf), torch.zeros(2, 4))
+    assert t.backward(torch.zeros(2, 64, **bf)).status is t.status
+    assert [n for n, _ in seen] == ["ragged_gemm"] * 3 + ["ragged_wgrad"] * 2 + ["ragged_gemm"]
+    assert all(word is t.status for _, word in seen)
+    t.check_status()
+    t.status.fill_(5)
+    with pytest.raises(_lib.Nvfp4Error, match="TIMEOUT"):
+        t.check_status()
+    t.check_status()                                   # reported once
+    with pytest.raises(RuntimeError, match="no forward_train"):
+        t.backward(torch.zeros(2, 64, **bf))
