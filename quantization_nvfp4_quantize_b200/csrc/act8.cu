@@ -111,7 +111,7 @@ __device__ __forceinline__ void store16(uint8_t *row, int64_t c, int64_t K, uint
 // padding of the scale row is written too).  Consecutive lanes take
 // consecutive items; the two lanes of a group always sit side by side because
 // `items` and the stride are even.
-__global__ void __launch_bounds__(THREADS, QUANT_BLOCKS) k_act8_quantize(const __nv_bfloat16 *__restrict__ x, int64_t M, int64_t K,
+__global__ void __launch_bounds__(THREADS, QUANT_BLOCKS) k_act8_quantize(const __nv_bfloat16 *x, int64_t M, int64_t K,
                                                            int64_t ldx, uint8_t *__restrict__ codes, int64_t ldc,
                                                            uint8_t *__restrict__ scales, int64_t lds, int items)
 {
@@ -155,9 +155,9 @@ __device__ __forceinline__ void decode4(uint32_t w, float v[4])
 // One item = 16 columns, as in the quantizer.  Every kept value is exact in
 // bf16.  Row r of the result is kept row src_rows[r] (null: r); an index
 // outside [0, T) gives zeros.
-__global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(const uint8_t *__restrict__ codes, int64_t ldc,
-                                                             const uint8_t *__restrict__ scales, int64_t lds,
-                                                             const int32_t *__restrict__ src_rows, int64_t T,
+__global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(const uint8_t *codes, int64_t ldc,
+                                                             const uint8_t *scales, int64_t lds,
+                                                             const int32_t *src_rows, int64_t T,
                                                              int64_t M, int64_t K, __nv_bfloat16 *__restrict__ x,
                                                              int64_t ldx, int items)
 {
@@ -226,7 +226,7 @@ __device__ __forceinline__ float2 sigmoid2(float2 a)
 
 // h = silu(gate) * up and both inputs kept: one item = 16 columns of gate and
 // the same 16 of up.
-__global__ void __launch_bounds__(THREADS, SWIGLU_BLOCKS) k_swiglu_act8(const __nv_bfloat16 *__restrict__ y, int64_t M, int64_t I,
+__global__ void __launch_bounds__(THREADS, SWIGLU_BLOCKS) k_swiglu_act8(const __nv_bfloat16 *y, int64_t M, int64_t I,
                                                          int64_t ldy, __nv_bfloat16 *__restrict__ h, int64_t ldh,
                                                          uint8_t *__restrict__ codes, int64_t ldc,
                                                          uint8_t *__restrict__ scales, int64_t lds, int items,
@@ -283,8 +283,8 @@ __global__ void __launch_bounds__(THREADS, SWIGLU_BLOCKS) k_swiglu_act8(const __
 // the row sum is a lane-ordered f32 sum and a fixed shuffle tree, so it does
 // not change from run to run.
 __global__ void __launch_bounds__(THREADS, BACKWARD_BLOCKS) k_swiglu_act8_backward(
-    const uint8_t *__restrict__ codes, int64_t ldc, const uint8_t *__restrict__ scales, int64_t lds,
-    const __nv_bfloat16 *__restrict__ dh, int64_t lddh, const float *__restrict__ row_gate, int64_t M, int64_t I,
+    const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds,
+    const __nv_bfloat16 *dh, int64_t lddh, const float *row_gate, int64_t M, int64_t I,
     __nv_bfloat16 *__restrict__ dy, int64_t lddy, __nv_bfloat16 *__restrict__ gh, int64_t ldgh,
     float *__restrict__ dgate)
 {
@@ -340,9 +340,9 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_BLOCKS) k_swiglu_act8_backwa
 // out[t] = sum_j g[t,j] rows[dst_row[t,j]] in slot order (f32): the routed
 // rows of a token brought back together, without atomics.  One thread per 8
 // columns of a token.
-__global__ void __launch_bounds__(THREADS) k_combine_rows(const __nv_bfloat16 *__restrict__ rows, int64_t M, int64_t H,
-                                                          int64_t ldr, const int32_t *__restrict__ dst_row,
-                                                          const float *__restrict__ gate, int kr,
+__global__ void __launch_bounds__(THREADS) k_combine_rows(const __nv_bfloat16 *rows, int64_t M, int64_t H,
+                                                          int64_t ldr, const int32_t *dst_row,
+                                                          const float *gate, int kr,
                                                           float *__restrict__ out, int64_t ldo)
 {
     grid_wait();
@@ -371,10 +371,10 @@ __global__ void __launch_bounds__(THREADS) k_combine_rows(const __nv_bfloat16 *_
 
 // Gradient of gates = softmax over the selected logits: one warp per token.
 //   dlogits[t, e] = sum over slots j with idx_j = e of g_j (d_j - sum_i g_i d_i)
-__global__ void __launch_bounds__(THREADS) k_route_backward(const int32_t *__restrict__ idx,
-                                                            const float *__restrict__ gate,
-                                                            const int32_t *__restrict__ dst_row,
-                                                            const float *__restrict__ dgate_row, int64_t M, int64_t T,
+__global__ void __launch_bounds__(THREADS) k_route_backward(const int32_t *idx,
+                                                            const float *gate,
+                                                            const int32_t *dst_row,
+                                                            const float *dgate_row, int64_t M, int64_t T,
                                                             int E, int kr, float *__restrict__ dlogits)
 {
     grid_wait();

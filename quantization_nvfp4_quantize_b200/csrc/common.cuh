@@ -92,6 +92,9 @@ __host__ __device__ __forceinline__ int64_t sf_bytes(int64_t rows, int64_t K) { 
 // global memory; grid_wait() returns when the predecessor has finished and its
 // writes are visible.  grid_release() lets the successor's blocks start once
 // every block of this grid has called it (they wait in grid_wait() themselves).
+// The predecessor still writes while such a kernel is resident, so its inputs are
+// not read-only for the kernel's lifetime: no const __restrict__ pointers, __ldg
+// or ld.global.nc in it (outputs may be __restrict__).
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

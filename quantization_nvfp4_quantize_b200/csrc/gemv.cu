@@ -214,10 +214,16 @@ __device__ __forceinline__ void copy4(void *dst, const void *src)
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
 }
 
+// 16 bytes of x.
+__device__ __forceinline__ void load16(const __nv_bfloat16 *src, uint4 &a)
+{
+    asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w) : "l"(src));
+}
+
 // 32 bytes of x (32-byte aligned).
 __device__ __forceinline__ void load32(const __nv_bfloat16 *src, uint4 &a, uint4 &b)
 {
-    asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+    asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
                  : "l"(src));
 }
@@ -275,7 +281,7 @@ __device__ __forceinline__ void dot_range(Slot<SETS> *ring, const Set (&l)[SETS]
             load32(px + 16, v[2], v[3]);
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = __ldg(reinterpret_cast<const uint4 *>(px) + k);
+            for (int k = 0; k < 4; ++k) load16(px + 8 * k, v[k]);
         }
     };
 #pragma unroll
@@ -510,8 +516,8 @@ __global__ void __launch_bounds__(32 * COMBINE_WARPS, 2) k_nvfp4_gemv_combine(co
 // out[t, n] = sum_j gate[t, j] y[t k_r + j, n], in slot order; a slot whose
 // expert does not exist takes no part, whatever its gate holds (as in the
 // one-launch form).
-__global__ void __launch_bounds__(THREADS) k_gemv_combine(const float *__restrict__ y, const float *__restrict__ gate,
-                                                          const int32_t *__restrict__ idx, int E, int k_r, int64_t N,
+__global__ void __launch_bounds__(THREADS) k_gemv_combine(const float *y, const float *gate,
+                                                          const int32_t *idx, int E, int k_r, int64_t N,
                                                           float *__restrict__ out, int64_t ld_out)
 {
     const int64_t n = (int64_t)blockIdx.x * THREADS + threadIdx.x;

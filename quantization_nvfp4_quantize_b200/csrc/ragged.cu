@@ -772,7 +772,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
 }
 
 // out = sum over splits of the partial results, in split order (+ out).
-__global__ void __launch_bounds__(256) k_wgrad_reduce(const float *__restrict__ part, int splits, int64_t n, void *out,
+__global__ void __launch_bounds__(256) k_wgrad_reduce(const float *part, int splits, int64_t n, void *out,
                                                       int out_f32, int accumulate)
 {
     const int64_t stride = (int64_t)gridDim.x * 256;

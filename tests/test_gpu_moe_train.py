@@ -349,3 +349,27 @@ def test_status_of_a_step(cuda):
     lay.forward_train(x, logits)
     assert torch.equal(lay.backward(dy).dx, g.dx)
     lay.check_status()
+
+
+def test_reused_buffers_are_never_read_stale(cuda):
+    """Steps back to back through the same buffers with new data each time:
+    every step's results are those of the step alone."""
+    T, E, H, I, kr = 48, 8, 128, 64, 2
+    lay, _, _ = layer(MoELayerW4A16, T, E, H, I, kr)
+    dec, _, _ = layer(MoELayerW4A4, 64, E, 256, 256, kr, 0)
+    steps = [(rnd(100 + i, T, H), rnd(200 + i, T, E, dtype=torch.float32), rnd(300 + i, T, H), rnd(400 + i, 6, 256),
+              rnd(500 + i, 6, E, dtype=torch.float32)) for i in range(12)]
+
+    def run(x, logits, dy, xd, ld):
+        y = lay.forward_train(x, logits)
+        g = lay.backward(dy)
+        return y, g.dx, g.dlogits, g.dw13, g.dw2, dec.decode(xd, ld)
+
+    want = []
+    for s in steps:
+        want.append(run(*s))
+        torch.cuda.synchronize()
+    for _ in range(5):
+        got = [run(*s) for s in steps]
+        for a, b in zip(got, want):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))

@@ -371,3 +371,18 @@ def test_training_pair_reports_waits_that_ran_out(monkeypatch):
     t.check_status()                                   # reported once
     with pytest.raises(RuntimeError, match="no forward_train"):
         t.backward(torch.zeros(2, 64, **bf))
+
+
+def test_overlapped_kernels_read_coherently():
+    """A kernel that starts before its predecessor has finished may not load
+    what that one writes as read-only data (the non-coherent path)."""
+    import glob
+    import os
+    import re
+    csrc = os.path.join(os.path.dirname(_lib.__file__), "csrc")
+    files = [f for f in glob.glob(os.path.join(csrc, "*.cu")) if "grid_wait()" in open(f).read()]
+    assert {os.path.basename(f) for f in files} >= {"act8.cu", "gemv.cu", "ragged.cu"}
+    for f in files:
+        code = re.sub(r"//[^\n]*", "", open(f).read())
+        found = re.findall(r"const\s+\w+\s*\*\s*__restrict__|__ldg\s*\(|ld\.global\.nc\b[^\"]*", code)
+        assert not found, (os.path.basename(f), found)
