@@ -721,7 +721,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     for (int c = 0; c < 128; c += 32) {
                         uint32_t x[32];
                         ptx::tmem_ld_32x32b_x32(src0 + (uint32_t)(acc * TILE + c), x);
-                        ptx::tmem_ld_wait();
+                        ptx::tmem_ld_wait(x);
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[c + i] += __uint_as_float(x[i]);
                     }

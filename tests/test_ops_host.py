@@ -386,3 +386,11 @@ def test_overlapped_kernels_read_coherently():
         code = re.sub(r"//[^\n]*", "", open(f).read())
         found = re.findall(r"const\s+\w+\s*\*\s*__restrict__|__ldg\s*\(|ld\.global\.nc\b[^\"]*", code)
         assert not found, (os.path.basename(f), found)
+
+
+def test_accumulator_loads_are_tied_to_their_wait():
+    """While another TMEM load is under way only the wait's own registers may be
+    used: the ragged products name them."""
+    import os
+    code = open(os.path.join(os.path.dirname(_lib.__file__), "csrc", "ragged.cu")).read()
+    assert "tmem_ld_wait(" in code and "tmem_ld_wait()" not in code
