@@ -169,17 +169,26 @@ def empty_routing(T: int, k_r: int, E: int, device, m_pad_max: int | None = None
                    m_pad_max, seg_align)
 
 
+def check_logits(what: str, logits: torch.Tensor):
+    """moe_route reads them through a bare pointer."""
+    if logits.dtype != F32 or logits.dim() != 2 or not logits.is_contiguous():
+        raise ValueError(f"{what}: logits must be contiguous f32 [T, E], got {logits.dtype} {list(logits.shape)}"
+                         f"{'' if logits.is_contiguous() else ', not contiguous'}")
+
+
 def route(logits: torch.Tensor, k_r: int, m_pad_max: int | None = None, seg_align: int = 128, *,
           out: Routing | None = None, workspace: torch.Tensor | None = None) -> Routing:
     """moe_route (see the header) on f32 logits [T, E].  `out` (empty_routing of
     the same sizes; its m_pad_max and seg_align are used) and `workspace` keep
     the call free of allocations."""
     lib = _lib.load()
-    assert logits.dtype == F32 and logits.is_contiguous()
+    check_logits("route", logits)
     T, E = logits.shape
     dev = logits.device
     r = empty_routing(T, k_r, E, dev, m_pad_max, seg_align) if out is None else out
-    assert tuple(r.topk_idx.shape) == (T, k_r) and r.offsets.numel() == E + 1
+    if tuple(r.topk_idx.shape) != (T, k_r) or r.offsets.numel() != E + 1:
+        raise ValueError(f"route: out is for {list(r.topk_idx.shape)} of {r.offsets.numel() - 1} experts, need "
+                         f"[{T}, {k_r}] of {E}")
     ws = _ws(lib.moe_route_workspace_size(T, E), dev) if workspace is None else workspace
     check(lib.moe_route(_p(logits), T, E, k_r, _p(r.topk_idx), _p(r.topk_gate), r.seg_align, _p(r.offsets), _p(r.dst_row),
                         _p(r.row_token), _p(r.row_gate), r.m_pad_max, _p(ws), ws.numel(), _stream(dev)))

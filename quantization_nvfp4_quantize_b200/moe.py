@@ -180,6 +180,7 @@ class MoELayerW4A4:
         if tuple(x.shape) != (logits.shape[0], self.H) or tuple(logits.shape) != (logits.shape[0], self.E):
             raise ValueError(f"decode: need x [t, {self.H}] and logits [t, {self.E}], got {tuple(x.shape)} and "
                              f"{tuple(logits.shape)}")
+        api.check_logits("decode", logits)
         if logits.shape[0] == 0:
             return torch.empty(0, self.H, dtype=torch.float32, device=x.device)
         with _current(x.device):
@@ -310,6 +311,7 @@ class MoELayerW4A16:
                              f"{tuple(x.shape)} and {tuple(logits.shape)}")
         if x.dtype != torch.bfloat16 or logits.dtype != torch.float32:
             raise ValueError(f"forward_train: x must be bf16 and logits f32, got {x.dtype} and {logits.dtype}")
+        api.check_logits("forward_train", logits)
         _same_device("forward_train", self.wq13, x=x, logits=logits)
         if not hasattr(self, "x8"):
             self._train_buffers(x.device)

@@ -394,3 +394,29 @@ def test_accumulator_loads_are_tied_to_their_wait():
     import os
     code = open(os.path.join(os.path.dirname(_lib.__file__), "csrc", "ragged.cu")).read()
     assert "tmem_ld_wait(" in code and "tmem_ld_wait()" not in code
+
+
+def test_logits_are_refused_without_asserts():
+    """Logits that a bare pointer would read wrongly: an error of its own, not
+    an assert that python -O takes out, and before anything is dropped."""
+    from quantization_nvfp4_quantize_b200.moe import MoELayerW4A4, MoELayerW4A16
+    good = torch.zeros(2, 4)
+    bad = [good.bfloat16(), good.double(), torch.zeros(4, 2).t(), torch.zeros(2, 8)[:, :4]]
+    t = MoELayerW4A16.__new__(MoELayerW4A16)
+    t.T, t.H, t.E, t.k_r, t.I, t.train_routing = 2, 64, 4, 2, 32, object()
+    t.wq13 = torch.empty(4, 64, 64, dtype=torch.bfloat16)
+    d = MoELayerW4A4.__new__(MoELayerW4A4)
+    d.H, d.E, d.c13 = 64, 4, torch.empty(4, 64, 32, dtype=torch.uint8)
+    x = torch.zeros(2, 64, dtype=torch.bfloat16)
+    for logits in bad:
+        with pytest.raises(ValueError, match="route: logits must be contiguous f32"):
+            api.route(logits, 2)
+        with pytest.raises(ValueError, match="decode: logits must be contiguous f32"):
+            d.decode(x, logits)
+        with pytest.raises(ValueError, match="logits"):
+            t.forward_train(x, logits)
+    assert t.train_routing is not None
+    with pytest.raises(ValueError, match="route: logits"):
+        api.route(torch.zeros(4), 2)
+    with pytest.raises(ValueError, match="route: out is for"):
+        api.route(good, 2, out=api.empty_routing(3, 2, 4, "cpu"))
