@@ -239,6 +239,9 @@ PyObject *ragged_wgrad(PyObject *const *v)
     const size_t need = ENTRY(WGRAD_WS, moe_ragged_wgrad_workspace_size)(M, N, K, (int32_t)E, kept);
     Tensor ws;
     if (need) ws = c.empty({(int64_t)need}, U8);
+    // a kept tensor without rows has no memory, but the library knows kept rows
+    // by their scales: any address does, nothing is read through it
+    if (kept && T == 0 && need) scales = static_cast<const uint8_t *>(ws.data_ptr());
     check(ENTRY(WGRAD, moe_ragged_wgrad)(g.data_ptr(), ldg, M, a.data_ptr(), lda, scales, lds, rows, T, N, K, (int32_t)E, off,
                                          out.data_ptr(), type == F32, accumulate, need ? ws.data_ptr() : nullptr, need,
                                          status_word(v[8], c), c.stream()));

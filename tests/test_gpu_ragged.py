@@ -424,3 +424,19 @@ def test_rows_of_no_kept_row_in_split_segments(cuda):
     got = api.ragged_wgrad(g, a8, off, a_rows=rows, out=old.clone(), accumulate=True)
     z = y + old.double()
     check(got, z, sum_bound(3500, s) + ULP_ADD * (y.abs() + old.double().abs()) + rounding(F32, z))
+
+
+def test_kept_tensor_without_rows(cuda):
+    """No row of g names a kept row: zeros, or the old value, even of NaN."""
+    off = offsets_of([20, 0, 100], cuda, start=1)
+    a8 = api.Act8.empty(0, 72, cuda)
+    g = torch.full((125, 24), float("nan"), dtype=BF16, device=cuda)
+    rows = torch.full((125,), -1, dtype=I32, device=cuda)
+    rows[50:] = 0
+    got = api.ragged_wgrad(g, a8, off, a_rows=rows)
+    assert tuple(got.shape) == (3, 24, 72) and not bool(got.any())
+    old = rnd(88, 3, 24, 72).float()
+    assert torch.equal(api.ragged_wgrad(g, a8, off, a_rows=rows, out=old.clone(), accumulate=True), old)
+    none = torch.zeros(4, dtype=I32, device=cuda)
+    assert not bool(api.ragged_wgrad(g[:0], a8, none, a_rows=rows[:0]).any())
+    assert not bool(api.ragged_wgrad(g[:0], a8, none).any())
