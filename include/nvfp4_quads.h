@@ -668,6 +668,14 @@ NVFP4_API nvfp4_status nvfp4_debug_ragged_wait_expiry(const void *a_dev, int64_t
                                                       int64_t ld_out, int32_t *dev_status, int64_t wait_limit_ns,
                                                       void *stream);
 
+/* nvfp4_debug_ragged_wgrad_wait_limit -- moe_ragged_wgrad (bf16 a, f32 out, no
+ * workspace) with every wait bounded at wait_limit_ns instead of 1 s: a test
+ * runs a segment that takes far longer and sees no timeout. */
+NVFP4_API nvfp4_status nvfp4_debug_ragged_wgrad_wait_limit(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev,
+                                                           int64_t lda, int64_t N, int64_t K, int32_t E,
+                                                           const int32_t *offsets_dev, void *out_dev,
+                                                           int32_t *dev_status, int64_t wait_limit_ns, void *stream);
+
 /* --------------------------------------------------------------------------
  * nvfp4_debug_encode -- runs the library's element and scale encoders on n
  * arbitrary floats (for validation against an independent definition):

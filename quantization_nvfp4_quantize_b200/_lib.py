@@ -92,6 +92,8 @@ SIGNATURES = {
                                  c_void_p]),
     "nvfp4_debug_ragged_wait_expiry": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_void_p,
                                                  c_void_p, c_int64, c_void_p, c_int64, c_void_p]),
+    "nvfp4_debug_ragged_wgrad_wait_limit": (c_int32, [c_void_p, c_int64, c_int64, c_void_p, c_int64, c_int64, c_int64,
+                                                      c_int32, c_void_p, c_void_p, c_void_p, c_int64, c_void_p]),
     "nvfp4_debug_gemm_wait_expiry": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
                                                c_int64, c_int64, c_int32, c_void_p, c_int32, c_void_p, c_void_p,
                                                c_void_p, c_int64, c_void_p, c_int64, c_void_p]),

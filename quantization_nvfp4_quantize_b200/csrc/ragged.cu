@@ -130,6 +130,7 @@ struct Shared {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
+    int progress;              // WGRAD: stages that the M-side producer has filled
     int dead[EPI_WARP0 + EPI_WARPS];   // INDEXED: the warp saw a row of no kept row
     int off[MAX_E + 1];        // segment bounds, made monotone and in [0, M]
     int tiles[MAX_E + 1];      // FWD / DGRAD: row tiles before expert e
@@ -137,18 +138,24 @@ struct Shared {
 
 // A converged warp's wait, bounded: false on a timeout or another role's.
 // `cluster`: the peer CTA's threads wrote shared memory before they arrived.
+// `progress`: while this count moves the bound starts anew (for a wait over
+// more than the stages in the ring).
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, const Params &p,
-                                         bool ignore_abort = false, bool cluster = false)
+                                         bool ignore_abort = false, bool cluster = false,
+                                         const volatile int *progress = nullptr)
 {
     bool ok = true;
     uint64_t t0 = 0;
+    int seen = 0;
     for (uint32_t i = 1;; ++i) {
         if (cluster ? ptx::mbar_try_wait_cluster(bar, parity) : ptx::mbar_try_wait_hint(bar, parity)) break;
         if ((i & 15u) == 0u) {
             if (!ignore_abort && *abort_flag) { ok = false; break; }
             const uint64_t now = globaltimer_ns();
-            if (t0 == 0) t0 = now;
-            else if (now - t0 > p.wait_limit_ns) {
+            if (t0 == 0 || (progress && *progress != seen)) {
+                t0 = now;
+                if (progress) seen = *progress;
+            } else if (now - t0 > p.wait_limit_ns) {
                 *abort_flag = 1;
                 report_status(p.dev_status, NVFP4_ERR_TIMEOUT);
                 ok = false;
@@ -411,6 +418,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
         }
         ptx::mbar_init(ptx::smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
+        sh->progress = 0;
         ptx::fence_mbar_init();
         ptx::fence_proxy_async_smem();
     }
@@ -499,6 +507,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
             if (one) ptx::prefetch_tmap(tm);
             uint32_t stage = 0, phase = 0;
             bool ok = true;
+            int filled = 0;
             for (Walk<MODE> at(p, unit, n_units); ok && at.t < total; at.next(p, n_units)) {
                 const Tile w = tile_at<MODE>(p, sh, at);
                 // this CTA's half of the operand
@@ -513,6 +522,7 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                         ok = false;
                         break;
                     }
+                    if (MODE == WGRAD && m_side && one) *(volatile int *)&sh->progress = ++filled;
                     const uint32_t dst = ptx::smem_u32(stage_base + stage * STAGE_BYTES + (m_side ? 0 : OPER_BYTES));
                     const uint32_t fb = ptx::smem_u32(&sh->full[stage]);
                     const uint32_t lfb = ptx::mapa_shared(fb, 0);      // the leader's barrier
@@ -648,7 +658,9 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     if (INDEXED && look) zero = dead_rows(p, row, w.r1);
                     if (row + BK > w.r1) zero |= ~0ull << (w.r1 - row);
                     if (zero == 0) continue;
-                    if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p)) {
+                    // the stage may lie a whole long segment, or many tiles, ahead
+                    if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p, false, false,
+                                  &sh->progress)) {
                         ok = false;
                         break;
                     }
@@ -934,11 +946,11 @@ extern "C" size_t moe_ragged_wgrad_workspace_size(int64_t M, int64_t N, int64_t 
     return (kept ? expanded_bytes(M, K) : 0) + (s > 1 ? (size_t)s * (size_t)E * (size_t)N * (size_t)K * 4 : 0);
 }
 
-extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev, int64_t lda,
-                                         const uint8_t *a_scales_dev, int64_t ld_scales, const int32_t *a_rows_dev,
-                                         int64_t T, int64_t N, int64_t K, int32_t E, const int32_t *offsets_dev,
-                                         void *out_dev, int32_t out_f32, int32_t accumulate, void *workspace,
-                                         size_t workspace_bytes, int32_t *dev_status, void *stream)
+static nvfp4_status ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev, int64_t lda,
+                                 const uint8_t *a_scales_dev, int64_t ld_scales, const int32_t *a_rows_dev, int64_t T,
+                                 int64_t N, int64_t K, int32_t E, const int32_t *offsets_dev, void *out_dev,
+                                 int32_t out_f32, int32_t accumulate, void *workspace, size_t workspace_bytes,
+                                 int32_t *dev_status, void *stream, uint64_t wait_limit_ns)
 {
     using namespace nvfp4::ragged;
     const bool kept = a_scales_dev != nullptr;
@@ -1003,7 +1015,7 @@ extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t
     p.m_tiles = (int)((K + TILE - 1) / TILE);
     p.n_tiles = (int)((N + TILE - 1) / TILE);
     p.splits = splits;
-    p.wait_limit_ns = TIMEOUT_NS;
+    p.wait_limit_ns = wait_limit_ns;
     p.offsets = offsets_dev;
     p.a_rows = a_rows_dev;
     p.kept_rows = T;
@@ -1025,4 +1037,25 @@ extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t
     launch_overlapped(k_wgrad_reduce, dim3(blocks), 256, 0, st, reinterpret_cast<const float *>(partials), splits, n, out_dev,
                       out_f32 ? 1 : 0, accumulate ? 1 : 0);
     return check_launch("k_wgrad_reduce");
+}
+
+extern "C" nvfp4_status moe_ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev, int64_t lda,
+                                         const uint8_t *a_scales_dev, int64_t ld_scales, const int32_t *a_rows_dev,
+                                         int64_t T, int64_t N, int64_t K, int32_t E, const int32_t *offsets_dev,
+                                         void *out_dev, int32_t out_f32, int32_t accumulate, void *workspace,
+                                         size_t workspace_bytes, int32_t *dev_status, void *stream)
+{
+    return ragged_wgrad(g_dev, ldg, M, a_dev, lda, a_scales_dev, ld_scales, a_rows_dev, T, N, K, E, offsets_dev, out_dev,
+                        out_f32, accumulate, workspace, workspace_bytes, dev_status, stream, nvfp4::ragged::TIMEOUT_NS);
+}
+
+extern "C" nvfp4_status nvfp4_debug_ragged_wgrad_wait_limit(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev,
+                                                            int64_t lda, int64_t N, int64_t K, int32_t E,
+                                                            const int32_t *offsets_dev, void *out_dev,
+                                                            int32_t *dev_status, int64_t wait_limit_ns, void *stream)
+{
+    NVFP4_REQUIRE(dev_status && wait_limit_ns >= 1000000 && wait_limit_ns <= 1000000000ll, NVFP4_ERR_INVALID_ARG,
+                  "nvfp4_debug_ragged_wgrad_wait_limit: needs dev_status and 1 ms <= wait_limit_ns <= 1 s");
+    return ragged_wgrad(g_dev, ldg, M, a_dev, lda, nullptr, 0, nullptr, 0, N, K, E, offsets_dev, out_dev, 1, 0, nullptr, 0,
+                        dev_status, stream, (uint64_t)wait_limit_ns);
 }

@@ -440,3 +440,33 @@ def test_kept_tensor_without_rows(cuda):
     none = torch.zeros(4, dtype=I32, device=cuda)
     assert not bool(api.ragged_wgrad(g[:0], a8, none, a_rows=rows[:0]).any())
     assert not bool(api.ragged_wgrad(g[:0], a8, none).any())
+
+
+def test_long_segment_under_a_short_wait_limit(cuda):
+    """The bound of a wait is on a stage that makes no progress, not on the time
+    to a far one: a segment of 2^25 + 5 rows (about 0.1 s) whose last, ragged
+    stage another warp waits for from the start, with every wait bounded at 5
+    ms.  Ones and small whole numbers: the sums are exact."""
+    from quantization_nvfp4_quantize_b200 import _lib
+    E, N, K, M = 75, 8, 8, 2 ** 25 + 5                             # enough experts for no row splits
+    off = torch.full((E + 1,), M, dtype=I32, device=cuda)
+    off[0] = 0
+    g = torch.zeros(M, N, dtype=BF16, device=cuda)
+    g[::64] = 1
+    a = torch.ones(M, K, dtype=BF16, device=cuda)
+    a[-1] = 2
+    g[-1] = 1
+    out = torch.full((E, N, K), 7.0, device=cuda)
+    status = torch.zeros(1, dtype=I32, device=cuda)
+    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, E, 0) == 0
+    p = api._p
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    assert _lib.load().nvfp4_debug_ragged_wgrad_wait_limit(p(g), N, M, p(a), K, N, K, E, p(off), p(out), p(status),
+                                                           5_000_000, api._stream(cuda)) == 0
+    end.record()
+    torch.cuda.synchronize()
+    assert api.read_status(status) == 0
+    want = float(g[:, 0].float().double().sum()) + 1               # the last row counts twice
+    assert bool((out[0] == want).all()) and not bool(out[1:].any())
+    assert start.elapsed_time(end) > 40                            # the case does what its name says

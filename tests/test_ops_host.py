@@ -420,3 +420,12 @@ def test_logits_are_refused_without_asserts():
         api.route(torch.zeros(4), 2)
     with pytest.raises(ValueError, match="route: out is for"):
         api.route(good, 2, out=api.empty_routing(3, 2, 4, "cpu"))
+
+
+def test_ragged_wgrad_wait_limit_arguments():
+    #       g     ldg  M    a     lda  N    K   E   off   out   stat  limit    stream
+    good = [FAKE, 256, 100, FAKE, 256, 256, 256, 128, FAKE, FAKE, FAKE, 2000000, None]
+    calls("nvfp4_debug_ragged_wgrad_wait_limit", good, [
+        (10, None, INVALID), (11, 999999, INVALID), (11, 1000000001, INVALID), (0, None, INVALID), (1, 248, ALIGN)])
+    # a result that needs a workspace
+    calls("nvfp4_debug_ragged_wgrad_wait_limit", [FAKE, 256, 5000, *good[3:7], 1, *good[8:]], [(11, 2000000, WORKSPACE)])
