@@ -75,7 +75,8 @@ def build_binding(force: bool = False) -> str:
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     """Compile csrc/*.cu and link libnvfp4_quads.so (returns its path), and
-    build the binding."""
+    build the binding.  The library needs nvcc alone: it is linked even where
+    the binding cannot be built, whose error is raised at the end."""
     os.makedirs(BUILD, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     if force:
@@ -84,12 +85,12 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs)) + 1) as ex:
         binding = ex.submit(build_binding, force)
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas), srcs))
+        if _stale(LIB, objs):
+            tmp = LIB + ".tmp%d" % os.getpid()
+            subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs,
+                                   "-lcudart"])
+            os.replace(tmp, LIB)
         binding.result()
-    if _stale(LIB, objs):
-        tmp = LIB + ".tmp%d" % os.getpid()
-        subprocess.check_call([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", tmp, *objs,
-                               "-lcudart"])
-        os.replace(tmp, LIB)
     return LIB
 
 

@@ -429,3 +429,25 @@ def test_ragged_wgrad_wait_limit_arguments():
         (10, None, INVALID), (11, 999999, INVALID), (11, 1000000001, INVALID), (0, None, INVALID), (1, 248, ALIGN)])
     # a result that needs a workspace
     calls("nvfp4_debug_ragged_wgrad_wait_limit", [FAKE, 256, 5000, *good[3:7], 1, *good[8:]], [(11, 2000000, WORKSPACE)])
+
+
+def test_library_is_linked_without_the_binding(monkeypatch, tmp_path):
+    """The C library needs neither torch's headers nor g++; a binding that
+    cannot be built is reported all the same."""
+    from quantization_nvfp4_quantize_b200 import build
+    lib = tmp_path / "lib.so"
+
+    def no_binding(force=False):
+        raise RuntimeError("no torch headers")
+
+    def link(cmd):
+        open(cmd[cmd.index("-o") + 1], "w").write("linked")
+
+    monkeypatch.setattr(build, "LIB", str(lib))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "build_binding", no_binding)
+    monkeypatch.setattr(build, "_compile", lambda src, verbose: src)
+    monkeypatch.setattr(build.subprocess, "check_call", link)
+    with pytest.raises(RuntimeError, match="no torch headers"):
+        build.build()
+    assert lib.read_text() == "linked"
