@@ -434,7 +434,8 @@ def test_ragged_wgrad_wait_limit_arguments():
 def test_library_is_linked_without_the_binding(monkeypatch, tmp_path):
     """The C library needs neither torch's headers nor g++; a binding that
     cannot be built is reported all the same."""
-    from quantization_nvfp4_quantize_b200 import build
+    import importlib
+    build = importlib.import_module("quantization_nvfp4_quantize_b200.build")
     lib = tmp_path / "lib.so"
 
     def no_binding(force=False):
