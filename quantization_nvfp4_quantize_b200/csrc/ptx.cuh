@@ -201,14 +201,6 @@ __device__ __forceinline__ void st_v4_f32(float *dst, float4 v)
                  : "memory");
 }
 
-// 32-byte vector store of eight 32-bit words (32-byte aligned).
-__device__ __forceinline__ void st_v8(void *dst, const uint32_t *v)
-{
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
-                 ::"l"(dst), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Wait until at most N of this thread's bulk groups are still reading shared
