@@ -240,3 +240,29 @@ def test_combine_skips_experts_that_do_not_exist(cuda, T, E, kr):
     got = run()
     assert bool(torch.isfinite(got).all())
     assert torch.equal(got, want)        # the sums' order goes by the slots, missing ones included
+
+
+@pytest.mark.parametrize("T,E,kr", [(1, 8, 8), (2, 128, 8), (3, 16, 5), (16, 32, 8), (300, 5, 4)])
+@pytest.mark.parametrize("N,K", [(8, 64), (130, 192), (96, 704), (258, 2048)])
+def test_whole_numbers(cuda, T, E, kr, N, K):
+    """Block and tensor scales of 1, whole x, gates that are powers of two: every
+    sum is exact, so one lost or doubled column, token or slot shows."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(40)
+    codes = torch.randint(0, 256, (E, N, K // 2), generator=gen, dtype=torch.uint8, device=cuda)
+    sf = torch.full((E, -(-N // 128) * 128 * (K // 16)), 0x38, dtype=torch.uint8, device=cuda)     # E4M3 1.0
+    s = torch.ones(E, device=cuda)
+    grid = torch.tensor([0, .5, 1, 1.5, 2, 3, 4, 6, 0, -.5, -1, -1.5, -2, -3, -4, -6], dtype=F64, device=cuda)
+    w = torch.stack([grid[(codes & 15).int()], grid[(codes >> 4).int()]], -1).view(E, N, K)
+    idx = torch.randint(-1, E + 1, (T, kr), generator=gen, device=cuda).to(I32)
+    flat = idx.view(-1).long()
+    live = ((flat >= 0) & (flat < E)).double()[:, None]
+    wf = w[flat.clamp(0, E - 1)]
+    x = torch.randint(-4, 5, (T, K), generator=gen, device=cuda).to(BF16)
+    y = torch.bmm(wf, x.double().repeat_interleave(kr, 0)[:, :, None])[:, :, 0] * live
+    assert torch.equal(api.nvfp4_gemv(x, codes, sf, s, N, K, expert_idx=idx).double(), y)
+    xc = torch.randint(-4, 5, (T * kr, K), generator=gen, device=cuda).to(BF16)
+    gate = torch.exp2(torch.randint(-2, 3, (T, kr), generator=gen, device=cuda).float())
+    y = torch.bmm(wf, xc.double()[:, :, None])[:, :, 0] * live * gate.double().view(-1, 1)
+    got = api.nvfp4_gemv(xc, codes, sf, s, N, K, expert_idx=idx, epilogue=api.EPI_COMBINE_F32, gate=gate)
+    assert torch.equal(got.double(), y.view(T, kr, N).sum(1))

@@ -470,3 +470,99 @@ def test_long_segment_under_a_short_wait_limit(cuda):
     want = float(g[:, 0].float().double().sum()) + 1               # the last row counts twice
     assert bool((out[0] == want).all()) and not bool(out[1:].any())
     assert start.elapsed_time(end) > 40                            # the case does what its name says
+
+
+def whole(seed, most, *shape):
+    """Whole numbers in [-most, most]: bf16 holds them, and every product and sum
+    of the tests below is exact in f32, in any order."""
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(seed)
+    return torch.randint(-most, most + 1, shape, generator=gen, device="cuda").to(BF16)
+
+
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("counts", COUNTS + [[1000, 511, 0, 513, 1]], ids=str)
+def test_products_of_whole_numbers(cuda, counts, transpose):
+    E, M, N, K = len(counts), sum(counts) + 9, 328, 520
+    off = offsets_of(counts, cuda, start=3)
+    w, a = whole(101, 3, E, N, K), whole(102, 4, M, N if transpose else K)
+    for dtype in (F32, BF16):
+        fill = torch.full((M, K if transpose else N), 7.0, dtype=dtype, device=cuda)
+        y, _ = ref_rows(a, w, off, transpose, fill)
+        assert torch.equal(api.ragged_gemm(a, w, off, transpose=transpose, out=fill), y.to(F32).to(dtype))
+
+
+def whole_gradients(g, a, off, av=None, **kw):
+    y, _ = ref_wgrad(g, a if av is None else av, off)
+    old = whole(103, 100, *y.shape).float()
+    for dtype in (F32, BF16):
+        assert torch.equal(api.ragged_wgrad(g, a, off, out_dtype=dtype, **kw), y.to(F32).to(dtype))
+        z = (y + old.double()).to(F32).to(dtype)
+        assert torch.equal(api.ragged_wgrad(g, a, off, out=old.to(dtype, copy=True), accumulate=True, **kw), z)
+
+
+@pytest.mark.parametrize("counts", COUNTS + [[1000, 511, 0, 513, 1], [4001, 64, 2500]], ids=str)
+@pytest.mark.parametrize("N,K", [(8, 8), (264, 72), (520, 328)])
+def test_weight_gradient_of_whole_numbers(cuda, counts, N, K):
+    """One lost, doubled or foreign row shows."""
+    M = sum(counts) + 9
+    g, a = whole(104, 2, M, N), whole(105, 3, M, K)
+    g[:2], a[:2], g[-7:], a[-7:] = float("nan"), float("inf"), float("nan"), float("inf")
+    whole_gradients(g, a, offsets_of(counts, cuda, start=2))
+
+
+@pytest.mark.parametrize("E,M,N,K", [(1, 20000, 64, 96), (3, 9001, 256, 264), (2, 5000, 300, 40), (1, 600, 8, 8),
+                                     (4, 30011, 8, 520)])
+def test_split_rows_of_whole_numbers(cuda, E, M, N, K):
+    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, E, 0) > 0
+    cuts = sorted([5] + [int(M * f) for f in (0.13, 0.52, 0.521)][: E - 1] + [M - 3])
+    off = torch.tensor(cuts, dtype=I32, device=cuda)
+    whole_gradients(whole(106, 2, M, -(-N // 8) * 8)[:, :N], whole(107, 3, M, K), off)
+
+
+@pytest.mark.parametrize("counts", COUNTS[1:] + [[4001, 64, 2500]], ids=str)
+@pytest.mark.parametrize("N,K", [(8, 8), (264, 333), (520, 528)])
+def test_kept_rows_of_whole_numbers(cuda, counts, N, K):
+    E, M, T = len(counts), sum(counts) + 4, 50
+    x = torch.zeros(T, -(-K // 8) * 8, dtype=BF16, device=cuda)[:, :K]
+    x.copy_(whole(108, 3, T, K))
+    a8 = api.act8_quantize(x)
+    assert torch.equal(kept_values(a8), x.double())                # 3 significant bits at most
+    rows = torch.randint(-2, T + 2, (M,), generator=torch.Generator().manual_seed(109)).to(I32).to(cuda)
+    ok = (rows >= 0) & (rows < T)
+    av = torch.where(ok[:, None], x.double()[rows.clamp(0, T - 1).long()], 0.0)
+    whole_gradients(whole(110, 2, M, N), a8, offsets_of(counts, cuda, start=1), av, a_rows=rows)
+
+
+def test_whole_numbers_behind_long_offsets(cuda):
+    """Rows whose element offsets pass 2^31, split over the SMs: exact."""
+    M, N, K = 1_100_000, 64, 2048
+    off = torch.tensor([M - 300, M - 100, M], dtype=I32, device=cuda)
+    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, 2, 0) > 0
+    a = torch.full((M, K), 3.0, dtype=BF16, device=cuda)
+    g = torch.full((M, N), 2.0, dtype=BF16, device=cuda)
+    a[-300:], g[-300:] = whole(111, 3, 300, K), whole(112, 2, 300, N)
+    y, _ = ref_wgrad(g[-300:], a[-300:], offsets_of([200, 100], cuda))
+    assert torch.equal(api.ragged_wgrad(g, a, off).double(), y)
+    w = whole(113, 3, 2, N, K)
+    y, _ = ref_rows(a[-300:], w, offsets_of([200, 100], cuda), False, torch.zeros(300, N, device=cuda))
+    assert torch.equal(api.ragged_gemm(a, w, off, out_dtype=F32)[-300:].double(), y)
+
+
+def test_weight_gradient_long_sums(cuda):
+    """131072 terms of one sign: at most 512 rows are summed on the tensor core.
+    32 MMAs of 16 exact products and the sum so far: 17 terms cut to the
+    largest's 24 bits each; then 256 additions in f32 (2^-24 each).  (One sum
+    over as many terms on the tensor core was seen to be off by more.)"""
+    E, N, K, M = 75, 16, 64, 131072                                # enough experts for no row splits
+    off = torch.full((E + 1,), M, dtype=I32, device=cuda)
+    off[0] = 0
+    g, a = rnd(114, M, N).abs(), rnd(115, M, K).abs()
+    assert api._lib.load().moe_ragged_wgrad_workspace_size(M, N, K, E, 0) == 0
+    bar = (32 * 17 + 256 + 1) * 2.0 ** -24
+    want = g.double().t() @ a.double()
+    got = api.ragged_wgrad(g, a, off)[0].double()
+    assert float(((got - want) / want).abs().max()) <= bar
+    # with the rows split over the SMs the parts are added in f32 as well
+    got = api.ragged_wgrad(g, a, off[[0, E]])[0].double()
+    assert float(((got - want) / want).abs().max()) <= bar + 64 * 2.0 ** -24
