@@ -298,7 +298,9 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_BLOCKS) k_swiglu_act8_backwa
         const float w = row_gate ? row_gate[row] : 1.0f;
         const float2 w2 = make_float2(w, w);
         float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll 3
+        // unrolled three times 47.1, twice 46.7, four times 46.9, not at all 46.0 us
+        // for 32768 x 768 (x 1536: 90.8, 91.6, 88.4, 87.7; x 256: 19.0, 16.5, 18.3, 17.4)
+#pragma unroll 1
         for (int64_t c = lane * 8; c < I; c += 256) {
             const uint2 ca = *reinterpret_cast<const uint2 *>(crow + c);
             const uint2 cb = *reinterpret_cast<const uint2 *>(crow + I + c);
