@@ -528,7 +528,8 @@ NVFP4_API nvfp4_status moe_w8a8_grouped_gemm(
  *                segments split over the SMs; otherwise 0.
  * Sums run in a fixed order: the same inputs give the same bits; at most 512
  * rows are summed on the tensor core at a time, the parts in f32.  E <= 256,
- * ldg % 8 == 0, lda % 8 == 0 (16 for codes), ld_scales % 4 == 0, any N and K.
+ * ldg % 8 == 0, lda % 8 == 0 (16 for codes), ld_scales % 4 == 0, any N and K; g, a
+ * and the scales 16-byte aligned, out aligned to its elements.
  *
  * Both: Inf and NaN stay in the rows (WGRAD: the segments) that hold them.
  * Timeouts as for moe_w4a4_grouped_gemm_rac (dev_status may be NULL).

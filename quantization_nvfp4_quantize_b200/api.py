@@ -368,7 +368,8 @@ def ragged_gemm(a: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, *, tran
     offsets[e+1]) times w[e]^T, or times w[e] with transpose (the input
     gradient).  a bf16 [M, K] (transpose: [M, N]), w bf16 [E, N, K].  Rows
     outside the segments are not written: pass `out` to keep what they hold
-    (without it they are uninitialized)."""
+    (without it they are uninitialized).  An f32 result shows the tensor core's
+    truncated additions: about 1.6e-6 in norm per 1024 terms."""
     return (_lib._bound or _lib.binding()).ragged_gemm(a, w, offsets, transpose, out, out_dtype, dev_status)
 
 
@@ -377,8 +378,10 @@ def ragged_wgrad(g: torch.Tensor, a, offsets: torch.Tensor, *, a_rows: torch.Ten
                  dev_status=None):
     """moe_ragged_wgrad (see the header): dw[e] = sum over the expert's rows of
     g[r]^T a[r].  g bf16 [M, N]; a bf16 [M, K], or an Act8 [T, K] whose row
-    a_rows[r] (int32 [M]; without it row r) belongs to row r.  accumulate adds
-    to `out`."""
+    a_rows[r] (int32 [M]; without it row r) belongs to row r; a row whose index
+    lies outside [0, T) adds nothing.  accumulate adds to `out` in place; for
+    large results that takes several times as long as a separate addition
+    (it waits for every old value in turn)."""
     b = _lib._bound or _lib.binding()
     if isinstance(a, Act8):
         return b.ragged_wgrad(g, a.codes, a.scales, offsets, a_rows, out, out_dtype, accumulate, dev_status)

@@ -13,10 +13,12 @@
 // NaN, so an overflow of the forward pass reaches the gradients.
 //
 // Every kernel here streams: one pass over the data, 16-byte loads and stores,
-// a resident grid.  The floor is HBM; measured with cold caches, launch
-// included: quantize 16384 x 4096 39 us (5.2 TB/s), SwiGLU keeping 32768 x 1536
-// 41 us (4.9 TB/s), its backward pass 53 us (4.8 TB/s).  What is left is load
-// latency and the encode: half of the issue slots and of the ALU pipe.
+// a resident grid.  The floor is HBM; measured in a loop over inputs larger than
+// L2: quantize 16384 x 4096 35 us (5.8 TB/s), expanding it again 36 us (5.7), SwiGLU
+// keeping 32768 rows of 2 x 768 columns 36 us (5.6), its backward pass 47 us (5.3),
+// the combine of 4096 tokens' 8 rows of 2048 31 us (5.4).  A single launch with a
+// cold L2 takes 4 to 6 us more.  What is left is load latency and the encode: half
+// of the issue slots and of the ALU pipe.
 #include "common.cuh"
 
 #include <algorithm>
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, BACKWARD_BLOCKS) k_swiglu_act8_backwa
         const float2 w2 = make_float2(w, w);
         float2 sum = make_float2(0.0f, 0.0f);
         // unrolled three times 47.1, twice 46.7, four times 46.9, not at all 46.0 us
-        // for 32768 x 768 (x 1536: 90.8, 91.6, 88.4, 87.7; x 256: 19.0, 16.5, 18.3, 17.4)
+        // for 32768 rows of I = 768 (1536: 90.8, 91.6, 88.4, 87.7; 256: 19.0, 16.5, 18.3, 17.4)
 #pragma unroll 1
         for (int64_t c = lane * 8; c < I; c += 256) {
             const uint2 ca = *reinterpret_cast<const uint2 *>(crow + c);

@@ -8,12 +8,17 @@
 //   WGRAD  dw_e[n, k] = sum_{r in e} g[r, n] a[r, k]
 //
 // Bound by the tensor pipe for segments of a few hundred rows and more, by the
-// weights' bytes below that (WGRAD: by the result's bytes).  Measured, one B200:
-//   FWD    one segment, 8192 x 4096 x 4096             172 us  1.60 PFLOP/s
-//          128 experts, 32768 rows, 2048 -> 1536       199 us  1.04 PFLOP/s, 5.2 TB/s
-//   DGRAD  32 experts, 32768 rows, 4096 -> 1536        287 us  1.44 PFLOP/s
-//   WGRAD  32 experts, 32768 rows, 4096 x 1536, f32    362 us  1.14 PFLOP/s, 3.2 TB/s
-//          128 experts, 32768 rows, 1536 x 2048, f32   336 us  0.61 PFLOP/s, 5.5 TB/s
+// weights' bytes below that (WGRAD: by the result's bytes).  Measured, one B200,
+// single launches with a cold L2, and in a continuous loop, which the power cap
+// slows (segments of a skewed router; with equal ones FWD of 128 experts takes
+// 211 us in the loop, so half of its distance to the bytes' 159 us is padding to
+// 64 rows and uneven work of the pairs):
+//   FWD    one segment, 8192 x 4096 x 4096             182 us  1.51 PFLOP/s
+//          128 experts, 32768 rows, 2048 -> 1536       210 us  0.98 PFLOP/s, 5.0 TB/s   loop 262 us
+//   DGRAD  32 experts, 32768 rows, 4096 -> 1536        300 us  1.37 PFLOP/s             loop 369 us
+//   WGRAD  32 experts, 32768 rows, 4096 x 1536, f32    375 us  1.10 PFLOP/s, 3.1 TB/s   loop 447 us
+//          128 experts, 32768 rows, 1536 x 2048, f32   347 us  0.59 PFLOP/s, 5.3 TB/s
+//          the same from kept rows                     390 us                           loop 440 us
 //
 // A cluster of two CTAs computes one tile with tcgen05 .cta_group::2: each CTA
 // stages half of the M-side operand (128 of 256) and half of the N-side one
@@ -61,7 +66,7 @@
 // (exact).  Converting inside the WGRAD kernel was built and measured: every
 // M-side tile converts its rows again, and 6 converter warps could not keep up
 // (1536 x 2048, 128 experts, 32768 rows: 731 us when a BF16 operand took 471;
-// with the expanded copy it is 375 against 336).
+// with the expanded copy it is 390 against 347).
 //
 // WGRAD with few output tiles splits every segment's rows over several tiles:
 // f32 partial results in the workspace, added in split order by a second
@@ -849,7 +854,12 @@ static nvfp4_status launch_wgrad(const CUtensorMap &tm_m, const CUtensorMap &tm_
 static int pair_stores(const void *base, int64_t ld) { return (reinterpret_cast<uintptr_t>(base) & 3u) == 0 && ld % 2 == 0; }
 
 // Row splits of a weight gradient: enough tiles for every CTA pair, but no
-// split shorter than 256 rows of an even segment.
+// split shorter than 256 rows of an even segment.  Measured without splits and
+// with them: one 256 x 256 result of 512 rows 9.1 and 9.7 us (two splits), of
+// 1024 11.5 and 9.6, of 32768 150 and 20; at least 128 or 512 rows a split the
+// same within 1 us.  With more tiles a second split gains less than its second
+// kernel costs: 5 experts of 520 x 264, 5000 rows, 14.0 and 15.1 us; 8 of 512 x
+// 512, 16384 rows, 17.0 and 20.4.
 static int wgrad_splits(int64_t M, int64_t N, int64_t K, int32_t E)
 {
     const int64_t tiles = ((N + TILE - 1) / TILE) * ((K + TILE - 1) / TILE) * E;
