@@ -523,9 +523,12 @@ NVFP4_API nvfp4_status moe_w8a8_grouped_gemm(
  *                accumulate: the sum of old value and gradient in f32, rounded
  *                once to out's type.
  *   workspace    moe_ragged_wgrad_workspace_size(M, N, K, E, kept) bytes, 16-byte
- *                aligned: kept (a in 8 bits): the kept rows in bf16, gathered
+ *                aligned: kept 1 (a in 8 bits): the kept rows in bf16, gathered
  *                into row order; a small result: f32 partial results of
- *                segments split over the SMs; otherwise 0.
+ *                segments split over the SMs; otherwise 0.  kept 2 (rows named
+ *                by a_rows): about 1 KB more, with which a_rows is looked
+ *                through for indices outside [0, T) once instead of by every
+ *                block; the size of kept 1 does too.
  * Sums run in a fixed order: the same inputs give the same bits; at most 512
  * rows are summed on the tensor core at a time, the parts in f32.  E <= 256,
  * ldg % 8 == 0, lda % 8 == 0 (16 for codes), ld_scales % 4 == 0, any N and K; g, a

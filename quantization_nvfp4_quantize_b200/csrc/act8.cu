@@ -156,12 +156,12 @@ __device__ __forceinline__ void decode4(uint32_t w, float v[4])
 
 // One item = 16 columns, as in the quantizer.  Every kept value is exact in
 // bf16.  Row r of the result is kept row src_rows[r] (null: r); an index
-// outside [0, T) gives zeros.
+// outside [0, T) gives zeros, and `outside` (where given) tells of it.
 __global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(const uint8_t *codes, int64_t ldc,
                                                              const uint8_t *scales, int64_t lds,
                                                              const int32_t *src_rows, int64_t T,
                                                              int64_t M, int64_t K, __nv_bfloat16 *__restrict__ x,
-                                                             int64_t ldx, int items)
+                                                             int64_t ldx, int items, uint8_t *__restrict__ outside)
 {
     grid_wait();
     grid_release();
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(con
     int item = (int)(first - row * items);
     const int64_t drow = stride / items;
     const int ditem = (int)(stride - drow * items);
+    bool met = false;
     while (row < M) {
         const int64_t c = (int64_t)item * 16;
         const int64_t from = src_rows ? (int64_t)src_rows[row] : row;
@@ -187,6 +188,8 @@ __global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(con
                 for (int i = 0; i < 16; ++i)
                     if (c + i < K) w[i >> 2] |= (uint32_t)src[i] << (8 * (i & 3));
             }
+        } else {
+            met = true;
         }
         uint32_t o[8];
 #pragma unroll
@@ -208,6 +211,10 @@ __global__ void __launch_bounds__(THREADS, DEQUANT_BLOCKS) k_act8_dequantize(con
         row += drow;
         item += ditem;
         if (item >= items) { item -= items; ++row; }
+    }
+    if (outside) {
+        const int any = __syncthreads_or(met);
+        if (threadIdx.x == 0) outside[blockIdx.x] = any != 0;
     }
 }
 
@@ -421,14 +428,18 @@ static unsigned stream_blocks(int64_t work, int resident)
 }  // namespace act8
 
 nvfp4_status act8_expand(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, const int32_t *rows,
-                         int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, cudaStream_t stream)
+                         int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, uint8_t *outside, int *blocks,
+                         cudaStream_t stream)
 {
     const int items = (int)((K + 15) / 16);
-    launch_overlapped(act8::k_act8_dequantize, act8::stream_blocks(M * items, act8::DEQUANT_BLOCKS), act8::THREADS, 0,
-                      stream, codes, ldc, scales, lds, rows, T, M, K, reinterpret_cast<__nv_bfloat16 *>(x), ldx,
-                      items);
+    const unsigned grid = act8::stream_blocks(M * items, act8::DEQUANT_BLOCKS);
+    if (blocks) *blocks = (int)grid;
+    launch_overlapped(act8::k_act8_dequantize, grid, act8::THREADS, 0, stream, codes, ldc, scales, lds, rows, T, M, K,
+                      reinterpret_cast<__nv_bfloat16 *>(x), ldx, items, outside);
     return check_launch("k_act8_dequantize");
 }
+
+int act8_expand_max_blocks() { return num_sms() * act8::DEQUANT_BLOCKS; }
 
 }  // namespace nvfp4
 
@@ -472,7 +483,8 @@ extern "C" nvfp4_status act8_dequantize(const uint8_t *codes_dev, int64_t ld_cod
     NVFP4_REQUIRE(ld_scales >= (K + 31) / 32, NVFP4_ERR_ALIGNMENT, "act8_dequantize: ld_scales must be >= ceil(K / 32)");
     NVFP4_REQUIRE(aligned16(x_dev) && aligned16(codes_dev), NVFP4_ERR_ALIGNMENT,
                   "act8_dequantize: pointers must be 16-byte aligned");
-    return act8_expand(codes_dev, ld_codes, scales_dev, ld_scales, nullptr, M, M, K, x_dev, ldx, (cudaStream_t)stream);
+    return act8_expand(codes_dev, ld_codes, scales_dev, ld_scales, nullptr, M, M, K, x_dev, ldx, nullptr, nullptr,
+                       (cudaStream_t)stream);
 }
 
 extern "C" nvfp4_status moe_swiglu_act8(const void *y_dev, int64_t M, int64_t I, int64_t ldy, void *h_dev, int64_t ldh,

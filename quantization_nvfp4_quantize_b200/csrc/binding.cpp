@@ -236,7 +236,7 @@ PyObject *ragged_wgrad(PyObject *const *v)
     c.on_gpu();
     const c10::cuda::CUDAGuard guard(c.dev);
     if (none(v[5])) out = c.empty({E, N, K}, type);
-    const size_t need = ENTRY(WGRAD_WS, moe_ragged_wgrad_workspace_size)(M, N, K, (int32_t)E, kept);
+    const size_t need = ENTRY(WGRAD_WS, moe_ragged_wgrad_workspace_size)(M, N, K, (int32_t)E, kept ? rows ? 2 : 1 : 0);
     Tensor ws;
     if (need) ws = c.empty({(int64_t)need}, U8);
     // a kept tensor without rows has no memory, but the library knows kept rows

@@ -41,9 +41,13 @@ bool make_tmap_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, uint
 
 // Rows of an 8-bit kept tensor (codes [T x ldc], scales [T x lds]) as bf16
 // [M x ldx]: row r is kept row rows[r] (null: r), zeros for an index outside
-// [0, T).  Arguments as act8_dequantize checks them.
+// [0, T).  Arguments as act8_dequantize checks them.  outside (or null): one
+// byte per block of the launch, at most act8_expand_max_blocks() of them: 1 if
+// the block met such an index, else 0; *blocks is their number.
 nvfp4_status act8_expand(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t lds, const int32_t *rows,
-                         int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, cudaStream_t stream);
+                         int64_t T, int64_t M, int64_t K, void *x, int64_t ldx, uint8_t *outside, int *blocks,
+                         cudaStream_t stream);
+int act8_expand_max_blocks();
 
 // The launch attribute that goes with grid_wait().
 inline cudaLaunchAttribute overlap_attribute()

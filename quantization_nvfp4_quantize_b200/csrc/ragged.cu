@@ -48,11 +48,12 @@
 // that stage lands on a barrier of its own CTA, warp 3 zeroes the surplus rows
 // of both operands in shared memory and only then reports the stage to the
 // MMA issuer.  A stage that holds a row whose index names no kept row goes the
-// same way: its row of a is zeros, but its row of g may be anything.  The row
-// index is looked through once at the start, and stage by stage only if it
-// holds such a row (1536 x 2048, 128 experts, 32768 rows: 432 -> 436 us without
-// one, 55 us more with a single one, twice the time with a third of all rows,
-// which one warp per CTA zeroes).  Ragged rows (FWD, DGRAD) need nothing: a
+// same way: its row of a is zeros, but its row of g may be anything.  Stages
+// look for such rows only if the expanding launch met one (1536 x 2048, 128
+// experts, 32768 rows: 55 us more with a single one, twice the time with a third
+// of all rows, which one warp per CTA zeroes).  Without room for that launch's
+// word every CTA looks through the whole row index first (one expert of 64 x 64,
+// 262144 rows: 43.7 -> 56.7 us).  Ragged rows (FWD, DGRAD) need nothing: a
 // surplus row only makes an accumulator column that the epilogue does not store.
 //
 // Long sums (WGRAD): the tensor core's f32 accumulation truncates, an error
@@ -118,6 +119,8 @@ struct Params {
     const int32_t *offsets;
     const int32_t *a_rows;     // INDEXED: kept row of each row
     int64_t kept_rows;         // INDEXED: rows of the kept tensor
+    const uint8_t *outside;    // INDEXED: what the expanding launch's blocks met (act8_expand), or null
+    int outside_n;
     void *out;
     int64_t ld_out;
     int pairs;                 // bf16 out: two neighbouring columns may be stored at once
@@ -483,9 +486,17 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
         if (lane == 31 && p.E == MAX_E) { sh->off[MAX_E] = last; sh->tiles[MAX_E] = incl; }
         if (INDEXED && lane == 0) sh->dead[warp] = 0;
     } else if (INDEXED) {
-        // the other warps look through the row index meanwhile: a routed batch
-        // without padding has no dead row, and then no stage looks again
-        const bool dead = any_dead_row(p, warp < FIX_WARP ? warp : warp - 1, EPI_WARP0 + EPI_WARPS - 1);
+        // the other warps ask meanwhile whether there is a dead row at all: a
+        // routed batch without padding has none, and then no stage looks
+        const int share = warp < FIX_WARP ? warp : warp - 1;
+        constexpr int SHARES = EPI_WARP0 + EPI_WARPS - 1;
+        bool dead = false;
+        if (p.outside) {
+            for (int i = share * 32 + lane; i < p.outside_n; i += SHARES * 32) dead |= p.outside[i] != 0;
+            dead = __any_sync(0xffffffffu, dead ? 1 : 0) != 0;
+        } else {
+            dead = any_dead_row(p, share, SHARES);
+        }
         if (lane == 0) sh->dead[warp] = dead;
     }
     grid_release();
@@ -659,10 +670,10 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     const uint32_t s = stage;
                     if (++stage == STAGES) stage = 0;
                     const int row = w.r0 + kb * BK;
-                    uint64_t zero = 0;
-                    if (INDEXED && look) zero = dead_rows(p, row, w.r1);
-                    if (row + BK > w.r1) zero |= ~0ull << (w.r1 - row);
-                    if (zero == 0) continue;
+                    const int rows = min(BK, w.r1 - row);
+                    uint64_t dead = 0;
+                    if (INDEXED && look) dead = dead_rows(p, row, w.r1);
+                    if (rows == BK && (!INDEXED || dead == 0)) continue;
                     // the stage may lie a whole long segment, or many tiles, ahead
                     if (!wait_bar(ptx::smem_u32(&sh->raw[s]), (parity >> s) & 1u, abort_flag, p, false, false,
                                   &sh->progress)) {
@@ -672,18 +683,15 @@ k_ragged_gemm(const __grid_constant__ CUtensorMap tm_m, const __grid_constant__ 
                     parity ^= 1u << s;
                     uint8_t *base = stage_base + s * STAGE_BYTES;
                     // 128-byte rows of both operands' boxes; the swizzle stays inside a row
-                    const int first = __ffsll((long long)zero) - 1;
-                    const auto zero_16 = [&](int i) {
+                    const auto zero_16 = [&](uint8_t *at) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b)
-                            *reinterpret_cast<uint4 *>(base + b * BOX_BYTES + i * 16) = make_uint4(0, 0, 0, 0);
+                        for (int b = 0; b < 4; ++b) *reinterpret_cast<uint4 *>(at + b * BOX_BYTES) = make_uint4(0, 0, 0, 0);
                     };
-                    if (!INDEXED || zero == ~0ull << first) {
-                        for (int i = 8 * first + lane; i < BK * 8; i += 32) zero_16(i);
-                    } else {
-                        for (int i = 8 * first + lane; i < BK * 8; i += 32)
-                            if (zero >> (i >> 3) & 1) zero_16(i);
+                    if (INDEXED && dead != 0) {
+                        for (int i = lane; i < rows * 8; i += 32)
+                            if (dead >> (i >> 3) & 1) zero_16(base + i * 16);
                     }
+                    for (int i = lane; i < (BK - rows) * 8; i += 32) zero_16(base + rows * 128 + i * 16);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_u32(&sh->full[s]), 0));
@@ -946,14 +954,17 @@ extern "C" nvfp4_status nvfp4_debug_ragged_wait_expiry(const void *a_dev, int64_
                        (uint64_t)wait_limit_ns, 1);
 }
 
-// Workspace of a weight gradient: [BF16 copy of the kept rows][partial results].
+// Workspace of a weight gradient: [BF16 copy of the kept rows][partial
+// results], and with rows named by an index, where there is room for it, [what
+// the expanding launch met].
 static size_t expanded_bytes(int64_t M, int64_t K) { return ((size_t)M * (size_t)((K + 7) / 8 * 8) * 2 + 255) / 256 * 256; }
 
 extern "C" size_t moe_ragged_wgrad_workspace_size(int64_t M, int64_t N, int64_t K, int32_t E, int32_t kept)
 {
     if (M <= 0 || N <= 0 || K <= 0 || E <= 0) return 0;
     const int s = nvfp4::ragged::wgrad_splits(M, N, K, E);
-    return (kept ? expanded_bytes(M, K) : 0) + (s > 1 ? (size_t)s * (size_t)E * (size_t)N * (size_t)K * 4 : 0);
+    return (kept ? expanded_bytes(M, K) : 0) + (s > 1 ? (size_t)s * (size_t)E * (size_t)N * (size_t)K * 4 : 0) +
+           (kept == 2 ? (size_t)nvfp4::act8_expand_max_blocks() : 0);
 }
 
 static nvfp4_status ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, const void *a_dev, int64_t lda,
@@ -1000,12 +1011,14 @@ static nvfp4_status ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, cons
 
     const int64_t max_tiles = (int64_t)E * ((K + TILE - 1) / TILE) * ((N + TILE - 1) / TILE) * splits;
     NVFP4_REQUIRE(max_tiles < (1ll << 30), NVFP4_ERR_UNSUPPORTED_SHAPE, "moe_ragged_wgrad: too many tiles");
-    uint8_t *partials = reinterpret_cast<uint8_t *>(workspace);
+    uint8_t *partials = reinterpret_cast<uint8_t *>(workspace), *outside = nullptr;
+    int outside_n = 0;
     if (kept) {
+        if (a_rows_dev && workspace_bytes >= moe_ragged_wgrad_workspace_size(M, N, K, E, 2)) outside = partials + need;
         // the kept rows as BF16, in row order
         const int64_t ld = (K + 7) / 8 * 8;
         const nvfp4_status rc = act8_expand(reinterpret_cast<const uint8_t *>(a_dev), lda, a_scales_dev, ld_scales,
-                                            a_rows_dev, T, M, K, workspace, ld, st);
+                                            a_rows_dev, T, M, K, workspace, ld, outside, &outside_n, st);
         if (rc != NVFP4_OK) return rc;
         a_dev = workspace;
         lda = ld;
@@ -1029,6 +1042,8 @@ static nvfp4_status ragged_wgrad(const void *g_dev, int64_t ldg, int64_t M, cons
     p.offsets = offsets_dev;
     p.a_rows = a_rows_dev;
     p.kept_rows = T;
+    p.outside = outside;
+    p.outside_n = outside_n;
     p.out = splits > 1 ? partials : out_dev;
     p.ld_out = K;
     p.pairs = pair_stores(p.out, K);

@@ -566,3 +566,33 @@ def test_weight_gradient_long_sums(cuda):
     # with the rows split over the SMs the parts are added in f32 as well
     got = api.ragged_wgrad(g, a, off[[0, E]])[0].double()
     assert float(((got - want) / want).abs().max()) <= bar + 64 * 2.0 ** -24
+
+
+def test_rows_of_no_kept_row_with_either_workspace(cuda):
+    """The C call with and without room for the expanding launch's word gives
+    the same bits, with and without such rows, from any alignment of the index."""
+    import ctypes
+
+    from quantization_nvfp4_quantize_b200 import _lib
+    lib, p = _lib.load(), api._p
+    M, T, N, K = 3001, 77, 264, 136
+    a8 = api.act8_quantize(rnd(120, T, K))
+    off = offsets_of([1000, 0, 1990], cuda, start=4)
+    for gone in ([], [2999], [5, 6, 1700], list(range(0, 3001, 3))):
+        for at in range(4):
+            rows = torch.zeros(M + 4, dtype=I32, device=cuda)[at:at + M]
+            rows.copy_(torch.randint(0, T, (M,), generator=torch.Generator().manual_seed(121)))
+            g = rnd(122, M, N, scale=0.1)
+            rows[gone] = -1
+            g[gone] = float("nan")
+            want = api.ragged_wgrad(g, a8, off, a_rows=rows)
+            assert bool(torch.isfinite(want).all())
+            sizes = [lib.moe_ragged_wgrad_workspace_size(M, N, K, 3, k) for k in (1, 2)]
+            assert 0 < sizes[1] - sizes[0] <= 4096
+            for size in sizes:
+                ws = torch.full((size + 64,), 0xFF, dtype=torch.uint8, device=cuda)
+                out = torch.empty(3, N, K, device=cuda)
+                assert lib.moe_ragged_wgrad(p(g), N, M, p(a8.codes), a8.codes.stride(0), p(a8.scales), a8.scales.stride(0),
+                                            p(rows), T, N, K, 3, p(off), p(out), 1, 0, p(ws), ctypes.c_size_t(size), None,
+                                            api._stream(cuda)) == 0
+                assert torch.equal(out, want) and bool((ws[size:] == 0xFF).all())
